@@ -13,7 +13,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libsgqa.so")
 SOURCES = ["api.cu", "merge.cu", "index_gemm.cu", "topk_union.cu", "select_long.cu", "attn.cu",
-           "attn_bwd.cu", "noalloc.cu"]
+           "attn_bwd.cu", "noalloc.cu", "paged_api.cu", "page_tables.cu", "paged_append.cu",
+           "paged_attn_simt.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 

@@ -1,0 +1,51 @@
+// New K and V rows into the paged pool through the slot map.
+#include "paged.h"
+
+namespace sgqa {
+namespace {
+
+// One warp per token: its K row and its V row, Hkv * d values each, move as
+// 16-byte units (up[] of them per head, a power of two).
+__global__ void __launch_bounds__(256)
+    k_paged_append(PagedDims pd, const uint4* __restrict__ K, const uint4* __restrict__ V,
+                   const int64_t* __restrict__ slot_map, uint4* __restrict__ Kp,
+                   uint4* __restrict__ Vp, int log_up, int64_t row_units, int32_t* status) {
+  const int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (t >= pd.T) return;
+  const int lane = threadIdx.x & 31;
+  const int64_t slot = slot_map[t];
+  if (slot < 0) return;
+  if (slot >= (int64_t)pd.n_pages * pd.ps) {
+    if (lane == 0) report(status, SGQA_ERR_BOUNDS, 321);
+    return;
+  }
+  const uint32_t page = (uint32_t)slot / (uint32_t)pd.ps, off = (uint32_t)slot % (uint32_t)pd.ps;
+  const int units = pd.Hkv << log_up;
+  const uint4* k = K + t * row_units;
+  const uint4* v = V + t * row_units;
+  const int64_t base = (int64_t)page * pd.Hkv * pd.ps + off;  // row of head 0
+  for (int u = lane; u < units; u += 32) {
+    const int g = u >> log_up, c = u & ((1 << log_up) - 1);
+    const int64_t at = ((base + (int64_t)g * pd.ps) << log_up) + c;
+    const uint4 x = k[u], y = v[u];
+    Kp[at] = x;
+    Vp[at] = y;
+  }
+}
+
+}  // namespace
+
+int launch_paged_append(const PagedDims& pd, const void* K, const void* V,
+                        const int64_t* slot_map, void* Kp, void* Vp, int32_t* status,
+                        cudaStream_t st) {
+  const int up = pd.d * pd.elem / 16;  // 8, 16 or 32
+  const int log_up = up == 8 ? 3 : up == 16 ? 4 : 5;
+  log_begin(SGQA_K_APPEND, st);
+  k_paged_append<<<(unsigned)((pd.T + 7) / 8), 256, 0, st>>>(
+      pd, static_cast<const uint4*>(K), static_cast<const uint4*>(V), slot_map,
+      static_cast<uint4*>(Kp), static_cast<uint4*>(Vp), log_up, pd.kvs * pd.elem / 16, status);
+  log_end(st);
+  return cudaGetLastError() == cudaSuccess ? SGQA_OK : SGQA_ERR_CUDA;
+}
+
+}  // namespace sgqa

@@ -35,13 +35,15 @@ EXPORTED = ("sgqa_workspace_bytes", "sgqa_union_capacity", "sgqa_block_merge", "
             "sgqa_topk_union", "sgqa_topk_union_noalloc", "sgqa_sparse_attn_fwd",
             "sgqa_sparse_attn_bwd", "sgqa_prefill", "sgqa_decode",
             "sgqa_prefill_ex", "sgqa_prefill_plan",
+            "sgqa_page_plan", "sgqa_page_release", "sgqa_paged_append",
+            "sgqa_paged_workspace_bytes", "sgqa_paged_attn",
             "sgqa_set_launch_log", "sgqa_reset_status", "sgqa_read_status", "sgqa_status_string",
             "sgqa_version")
 (K_MERGE, K_SPLIT, K_INDEX_QUERY, K_INDEX_SCORES, K_TOPK_UNION, K_ATTN, K_STAGE, K_TILE_UNION,
- K_SAMPLE_SCORES, K_ROW_TAU, K_ATTN_BWD) = (1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11)
+ K_SAMPLE_SCORES, K_ROW_TAU, K_ATTN_BWD, K_PAGES, K_APPEND, K_PAGED_ATTN) = range(1, 15)
 KERNEL_NAMES = {1: "merge", 2: "split", 3: "index_query", 4: "index_scores", 5: "topk_union",
                 6: "sparse_attn", 7: "stage_bf16", 8: "tile_union", 9: "sample_scores",
-                10: "row_tau", 11: "sparse_attn_bwd"}
+                10: "row_tau", 11: "sparse_attn_bwd", 12: "pages", 13: "append", 14: "paged_attn"}
 
 
 class Params(ctypes.Structure):
@@ -50,6 +52,17 @@ class Params(ctypes.Structure):
         "topk_tokens", "tile_q", "page_size", "dtype", "union_mode")] + [
         ("softmax_scale", ctypes.c_float), ("batch", ctypes.c_int32),
         ("index_mode", ctypes.c_int32)]
+
+    def as_dict(self):
+        return {n: getattr(self, n) for n, _ in self._fields_}
+
+
+class PagedParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "n_seqs", "max_tokens", "n_q_heads", "n_kv_heads", "head_dim", "page_size", "n_pages",
+        "max_pages", "dtype", "causal", "window")] + [
+        ("softmax_scale", ctypes.c_float), ("q_stride", ctypes.c_int32),
+        ("kv_stride", ctypes.c_int32)]
 
     def as_dict(self):
         return {n: getattr(self, n) for n, _ in self._fields_}
@@ -96,6 +109,13 @@ _lib.sgqa_prefill_ex.argtypes = [_P, _vp, _vp, _vp, ctypes.POINTER(IndexInputs),
 _lib.sgqa_decode.argtypes = [_P, _vp, _vp, _vp, _vp, ctypes.POINTER(BlockKeyCache), _vp, _vp, _vp,
                              _sz, _vp, _vp]
 _lib.sgqa_prefill_plan.argtypes = [_P, ctypes.POINTER(_i64), ctypes.POINTER(_i32)]
+_PP = ctypes.POINTER(PagedParams)
+_lib.sgqa_page_plan.argtypes = [_PP] + [_vp] * 11
+_lib.sgqa_page_release.argtypes = [_PP] + [_vp] * 8
+_lib.sgqa_paged_append.argtypes = [_PP] + [_vp] * 7
+_lib.sgqa_paged_workspace_bytes.argtypes = [_PP]
+_lib.sgqa_paged_workspace_bytes.restype = _sz
+_lib.sgqa_paged_attn.argtypes = [_PP] + [_vp] * 9 + [_sz, _vp, _vp]
 _lib.sgqa_set_launch_log.argtypes = [ctypes.POINTER(LaunchLog)]
 _lib.sgqa_reset_status.argtypes = [_vp, _vp]
 _lib.sgqa_read_status.argtypes = [_vp, ctypes.POINTER(_i32), _vp]
@@ -104,6 +124,7 @@ _lib.sgqa_status_string.restype = ctypes.c_char_p
 _lib.sgqa_version.restype = ctypes.c_int
 for _f in ("sgqa_block_merge", "sgqa_index_scores", "sgqa_topk_union", "sgqa_topk_union_noalloc",
            "sgqa_sparse_attn_fwd", "sgqa_sparse_attn_bwd",
+           "sgqa_page_plan", "sgqa_page_release", "sgqa_paged_append", "sgqa_paged_attn",
            "sgqa_prefill", "sgqa_prefill_ex", "sgqa_decode", "sgqa_prefill_plan", "sgqa_set_launch_log", "sgqa_reset_status",
            "sgqa_read_status"):
     getattr(_lib, _f).restype = ctypes.c_int
@@ -276,6 +297,127 @@ def sgqa_prefill_plan(p):
     _check(_lib.sgqa_prefill_plan(ctypes.byref(p), ctypes.byref(c), ctypes.byref(n)),
            "sgqa_prefill_plan")
     return int(c.value), int(n.value)
+
+
+# ------------------------------------------------------- ragged paged serving
+def paged_params(n_seqs, max_tokens, n_q_heads, n_kv_heads, head_dim, page_size, n_pages,
+                 max_pages, dtype=BF16, causal=True, window=0, softmax_scale=0.0, q_stride=0,
+                 kv_stride=0) -> PagedParams:
+    return PagedParams(n_seqs, max_tokens, n_q_heads, n_kv_heads, head_dim, page_size, n_pages,
+                       max_pages, dtype, int(causal), window, softmax_scale, q_stride, kv_stride)
+
+
+def paged_workspace_bytes(p: PagedParams) -> int:
+    return int(_lib.sgqa_paged_workspace_bytes(ctypes.byref(p)))
+
+
+def alloc_paged_workspace(p: PagedParams, device="cuda") -> torch.Tensor:
+    return torch.empty(max(paged_workspace_bytes(p), 1), dtype=torch.uint8, device=device)
+
+
+def paged_pool(p: PagedParams, device="cuda"):
+    """Zeroed (K_pages, V_pages) of the params' pool."""
+    shape = (p.n_pages, p.n_kv_heads, p.page_size, p.head_dim)
+    return (torch.zeros(shape, dtype=_odt(p), device=device),
+            torch.zeros(shape, dtype=_odt(p), device=device))
+
+
+_TORCH_DTYPE = {BF16: torch.bfloat16, FP32: torch.float32}
+
+
+def _at(t, dtype, numel, dev, what):
+    """Device address of a contiguous tensor of at least `numel` values of `dtype`."""
+    if t.dtype != dtype or t.device != dev or not t.is_contiguous() or t.numel() < numel:
+        raise ValueError(f"{what}: expected a contiguous {dtype} tensor of at least {numel} "
+                         f"values on {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _rows_at(t, p, heads, stride, dev, what):
+    """Device address of token rows [T][heads][d], packed but for the row stride."""
+    d = p.head_dim
+    if (t.dim() != 3 or t.dtype != _TORCH_DTYPE.get(p.dtype) or t.device != dev or
+            t.shape[0] < p.max_tokens or t.shape[1] != heads or t.shape[2] != d):
+        raise ValueError(f"{what}: expected [{p.max_tokens}][{heads}][{d}] in the params' dtype "
+                         f"on {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    want = stride or heads * d
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d) or (
+            t.shape[0] > 1 and t.stride(0) != want):
+        raise ValueError(f"{what}: strides {t.stride()} are not ({want}, {d}, 1) of the params")
+    return t.data_ptr()
+
+
+def _paged_call(fn, what, dev, stream, *args):
+    """The call on `dev`: its current stream unless one is given, and that
+    device current while the library launches."""
+    if dev.type != "cuda":
+        raise ValueError(f"{what}: expected CUDA tensors")
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _check(fn(*args, _stream(stream)), what)
+    _check(fn(*args, _stream(stream)), what)
+
+
+def _status_at(status, dev):
+    return None if status is None else _at(status, torch.int32, 4, dev, "status")
+
+
+def sgqa_page_plan(p, q_len, kv_len, free_pages, n_free, page_table, q_start, slot_map, positions,
+                   n_free_out, status=None, stream=None):
+    """Page table rows, q_start, slot_map and positions of a step from its lengths."""
+    dev, i32, n = kv_len.device, torch.int32, p.n_seqs
+    _paged_call(_lib.sgqa_page_plan, "sgqa_page_plan", dev, stream, ctypes.byref(p),
+                _at(q_len, i32, n, dev, "q_len"), _at(kv_len, i32, n, dev, "kv_len"),
+                _at(free_pages, i32, p.n_pages, dev, "free_pages"),
+                _at(n_free, i32, 1, dev, "n_free"),
+                _at(page_table, i32, n * p.max_pages, dev, "page_table"),
+                _at(q_start, i32, n + 1, dev, "q_start"),
+                _at(slot_map, torch.int64, p.max_tokens, dev, "slot_map"),
+                _at(positions, i32, p.max_tokens, dev, "positions"),
+                _at(n_free_out, i32, 1, dev, "n_free_out"), _status_at(status, dev))
+
+
+def sgqa_page_release(p, kv_len, keep_len, page_table, free_pages, n_free, n_free_out,
+                      status=None, stream=None):
+    """Pages past each request's keep_len pushed back on the free stack."""
+    dev, i32, n = kv_len.device, torch.int32, p.n_seqs
+    _paged_call(_lib.sgqa_page_release, "sgqa_page_release", dev, stream, ctypes.byref(p),
+                _at(kv_len, i32, n, dev, "kv_len"), _at(keep_len, i32, n, dev, "keep_len"),
+                _at(page_table, i32, n * p.max_pages, dev, "page_table"),
+                _at(free_pages, i32, p.n_pages, dev, "free_pages"),
+                _at(n_free, i32, 1, dev, "n_free"), _at(n_free_out, i32, 1, dev, "n_free_out"),
+                _status_at(status, dev))
+
+
+def _pool_at(t, p, dev, what):
+    return _at(t, _TORCH_DTYPE.get(p.dtype), p.n_pages * p.n_kv_heads * p.page_size * p.head_dim,
+               dev, what)
+
+
+def sgqa_paged_append(p, K, V, slot_map, K_pages, V_pages, status=None, stream=None):
+    """New K and V rows [T][Hkv][d] (row stride p.kv_stride) into the pool."""
+    dev = K_pages.device
+    _paged_call(_lib.sgqa_paged_append, "sgqa_paged_append", dev, stream, ctypes.byref(p),
+                _rows_at(K, p, p.n_kv_heads, p.kv_stride, dev, "K"),
+                _rows_at(V, p, p.n_kv_heads, p.kv_stride, dev, "V"),
+                _at(slot_map, torch.int64, p.max_tokens, dev, "slot_map"),
+                _pool_at(K_pages, p, dev, "K_pages"), _pool_at(V_pages, p, dev, "V_pages"),
+                _status_at(status, dev))
+
+
+def sgqa_paged_attn(p, Q, K_pages, V_pages, page_table, q_start, kv_len, O, lse, ws, status=None,
+                    stream=None):
+    """Attention of the step's tokens [T][H][d] over the paged pool: O and lse."""
+    dev, i32, n = K_pages.device, torch.int32, p.n_seqs
+    _paged_call(_lib.sgqa_paged_attn, "sgqa_paged_attn", dev, stream, ctypes.byref(p),
+                _rows_at(Q, p, p.n_q_heads, p.q_stride, dev, "Q"),
+                _pool_at(K_pages, p, dev, "K_pages"), _pool_at(V_pages, p, dev, "V_pages"),
+                _at(page_table, i32, n * p.max_pages, dev, "page_table"),
+                _at(q_start, i32, n + 1, dev, "q_start"), _at(kv_len, i32, n, dev, "kv_len"),
+                _at(O, _TORCH_DTYPE.get(p.dtype), p.max_tokens * p.n_q_heads * p.head_dim, dev,
+                    "O"),
+                _at(lse, torch.float32, p.n_q_heads * p.max_tokens, dev, "lse"),
+                _at(ws, torch.uint8, 0, dev, "ws"), ws.numel(), _status_at(status, dev))
 
 
 class launch_log:

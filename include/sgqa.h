@@ -362,6 +362,115 @@ SGQA_API int sgqa_decode(const sgqa_params* p, const void* Q, const void* K, con
                          float* lse, void* ws, size_t ws_bytes, int32_t* status,
                          sgqa_stream_t stream);
 
+/* --------------------------------------------------------------------------
+ * Ragged serving batches over one paged K/V pool: page tables and slot maps,
+ * the write of new K and V rows, and attention of the new tokens (the dense
+ * and sliding-window layers beside the sparse one, and its dense limit).
+ * All lengths live on the device, so one captured graph serves every step.
+ *
+ * N = n_seqs requests share the pool K_pages, V_pages [n_pages][n_kv_heads]
+ * [page_size][head_dim].  Row s of page_table [N][max_pages] lists the pages
+ * of request s in order; its entries from ceil(kv_len[s] / page_size) on are
+ * never read.  kv_len [N] counts the positions in the cache at the end of the
+ * step, its new tokens included.  The new tokens of the whole batch lie one
+ * request after another: those of request s are rows q_start[s] ..
+ * q_start[s + 1] - 1 of Q, K, V, O, slot_map and positions, and row
+ * q_start[s] + i sits at position kv_len[s] - q_len[s] + i.  max_tokens is
+ * the number of rows those tensors have, at least q_start[N]; rows from
+ * q_start[N] on are padding.
+ * Supported: head_dim 64 and 128, page_size a multiple of 8, n_q_heads /
+ * n_kv_heads up to 128, max_tokens up to 2^24, max_pages * page_size up to
+ * 2^30 positions, n_pages * n_kv_heads * page_size below 2^31
+ * (SGQA_ERR_UNSUPPORTED otherwise). */
+typedef struct sgqa_paged_params {
+  int32_t n_seqs;       /* N >= 0 */
+  int32_t max_tokens;   /* rows of Q, K, V, O, slot_map and positions, >= 0 */
+  int32_t n_q_heads;    /* H, a multiple of n_kv_heads */
+  int32_t n_kv_heads;   /* Hkv >= 1 */
+  int32_t head_dim;     /* d: 64 or 128 */
+  int32_t page_size;    /* positions per page */
+  int32_t n_pages;      /* pages of the pool, >= 1 */
+  int32_t max_pages;    /* columns of page_table, >= 1 */
+  int32_t dtype;        /* enum sgqa_dtype of Q, K, V, O and the pool */
+  int32_t causal;       /* 1: a token sees positions up to its own; 0: all kv_len */
+  int32_t window;       /* > 0 (causal only): the last `window` positions, its own
+                           included; 0: no limit */
+  float softmax_scale;  /* 0 -> 1 / sqrt(head_dim) */
+  int32_t q_stride;     /* elements between rows of Q (0 -> H * d); heads are packed */
+  int32_t kv_stride;    /* elements between rows of K and of V (0 -> Hkv * d) */
+} sgqa_paged_params;
+
+/* Page tables and slot maps of a step, from its lengths.  Request s held
+ * ceil((kv_len[s] - q_len[s]) / page_size) pages and needs ceil(kv_len[s] /
+ * page_size); the new ones are taken from the top of the stack free_pages
+ * [n_pages], of which the first n_free[0] entries are free, in the order of
+ * requests and positions: the k-th new page of the call is
+ * free_pages[n_free[0] - 1 - k].  Writes the new entries of page_table (no
+ * others), q_start [N + 1], slot_map [max_tokens] (page * page_size + offset
+ * of each new token; -1 for padding rows), positions [max_tokens] (-1 for
+ * padding) and n_free_out[0].  free_pages is only read, so a repeated call
+ * with the same inputs repeats its outputs; n_free and n_free_out are two
+ * buffers (INVALID_ARG if they are one).
+ * A step that does not fit takes nothing: q_start becomes all 0, slot_map and
+ * positions all -1, n_free_out = n_free and page_table stays; the status word
+ * gets SGQA_ERR_CAPACITY (too few free pages, more than max_tokens tokens) or
+ * SGQA_ERR_BOUNDS (a negative length, kv_len < q_len, kv_len > max_pages *
+ * page_size, n_free outside [0, n_pages]).  A page number outside the pool
+ * gives slot -1 and SGQA_ERR_BOUNDS. */
+SGQA_API int sgqa_page_plan(const sgqa_paged_params* p, const int32_t* q_len,
+                            const int32_t* kv_len, const int32_t* free_pages,
+                            const int32_t* n_free, int32_t* page_table, int32_t* q_start,
+                            int64_t* slot_map, int32_t* positions, int32_t* n_free_out,
+                            int32_t* status, sgqa_stream_t stream);
+
+/* Give pages back: request s, which holds ceil(kv_len[s] / page_size) pages,
+ * keeps those of its first keep_len[s] positions (0: it ended; less than
+ * kv_len: positions taken back).  The others are pushed on the stack in the
+ * order of requests and positions: the k-th goes to free_pages[n_free[0] + k];
+ * n_free_out[0] = n_free[0] + their number.  page_table is only read.  Pages
+ * that several requests share must be given back once, by one of them.
+ * SGQA_ERR_BOUNDS (keep_len outside [0, kv_len], kv_len above max_pages *
+ * page_size, n_free outside [0, n_pages]) and SGQA_ERR_CAPACITY (more pages
+ * than the stack's n_pages entries) change nothing but n_free_out = n_free. */
+SGQA_API int sgqa_page_release(const sgqa_paged_params* p, const int32_t* kv_len,
+                               const int32_t* keep_len, const int32_t* page_table,
+                               int32_t* free_pages, const int32_t* n_free, int32_t* n_free_out,
+                               int32_t* status, sgqa_stream_t stream);
+
+/* Write the rows K, V [max_tokens][Hkv][d] (row stride kv_stride) of the new
+ * tokens into the pool: row t goes to position slot_map[t] % page_size of page
+ * slot_map[t] / page_size.  Rows with a negative slot are skipped, slots of
+ * n_pages * page_size or more too (SGQA_ERR_BOUNDS).  The values are copied
+ * bit for bit.  Two rows with the same slot leave an unspecified mix of both. */
+SGQA_API int sgqa_paged_append(const sgqa_paged_params* p, const void* K, const void* V,
+                               const int64_t* slot_map, void* K_pages, void* V_pages,
+                               int32_t* status, sgqa_stream_t stream);
+
+/* Attention of the step's tokens over the paged cache, for prompts, chunks of
+ * them and single tokens in one call: token t of request s, head h of KV group
+ * h / G: softmax over the visible positions j of scale * Q[t][h] . K[j], times
+ * V[j].  Visible: j < kv_len[s]; with causal also j <= pos(t); with a window
+ * also j > pos(t) - window.  O [max_tokens][H][d]; lse [H][max_tokens] fp32,
+ * the natural log of the softmax denominator.  A token that sees nothing (a
+ * position below 0, an empty cache) gets O = 0 and lse = -inf; padding rows
+ * of O and lse are not written.  Positions from kv_len on, and positions no
+ * row of a 128-row query tile can see because of the window, are never read
+ * or have no effect whatever they hold, and neither do page_table entries of
+ * pages that hold only such positions.  bf16 runs on the tensor cores (fp32
+ * softmax and accumulation, the softmax weights rounded to bf16 for their
+ * product with V); fp32 runs in fp32 throughout.
+ * Device checks (SGQA_ERR_BOUNDS): kv_len outside [0, max_pages * page_size]
+ * and q_start that decreases or leaves [0, max_tokens] drop the request, a
+ * page number outside the pool reads as zeros.  Results do not depend on
+ * scheduling: two calls on the same inputs agree bit for bit.
+ * Workspace: sgqa_paged_workspace_bytes(p); calls that may overlap need one
+ * each. */
+SGQA_API size_t sgqa_paged_workspace_bytes(const sgqa_paged_params* p);
+SGQA_API int sgqa_paged_attn(const sgqa_paged_params* p, const void* Q, const void* K_pages,
+                             const void* V_pages, const int32_t* page_table,
+                             const int32_t* q_start, const int32_t* kv_len, void* O, float* lse,
+                             void* ws, size_t ws_bytes, int32_t* status, sgqa_stream_t stream);
+
 /* Plan of one sgqa_prefill call: queries per chunk (*chunk_queries) and the
  * number of kernel launches it enqueues (*launches).  Either pointer may be
  * NULL.  Returns an sgqa_status_code. */
@@ -379,7 +488,10 @@ enum sgqa_kernel_kind {
   SGQA_K_TILE_UNION = 8,   /* tile union and member masks */
   SGQA_K_SAMPLE_SCORES = 9, /* indexer GEMM over the sampled blocks (fused prefill) */
   SGQA_K_ROW_TAU = 10,      /* candidate thresholds from the sampled scores */
-  SGQA_K_ATTN_BWD = 11      /* attention backward (dQ; dK and dV) */
+  SGQA_K_ATTN_BWD = 11,     /* attention backward (dQ; dK and dV) */
+  SGQA_K_PAGES = 12,        /* page tables and slot maps; page release */
+  SGQA_K_APPEND = 13,       /* K/V rows written into the paged pool */
+  SGQA_K_PAGED_ATTN = 14    /* ragged attention over the paged pool, and its merge */
 };
 
 /* Optional launch log for measurement.  While a log is installed, every
