@@ -14,7 +14,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libsgqa.so")
 SOURCES = ["api.cu", "merge.cu", "index_gemm.cu", "topk_union.cu", "select_long.cu", "attn.cu",
            "attn_bwd.cu", "noalloc.cu", "paged_api.cu", "page_tables.cu", "paged_append.cu",
-           "paged_attn_simt.cu"]
+           "paged_attn_simt.cu", "paged_attn_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 

@@ -44,6 +44,10 @@ struct PagedAttnArgs {
 size_t paged_simt_ws_bytes(const PagedDims& pd);
 int launch_paged_simt(const PagedDims& pd, const PagedAttnArgs& a, void* ws, cudaStream_t st);
 
+// tensor-core attention (bf16)
+size_t paged_tc_ws_bytes(const PagedDims& pd);
+int launch_paged_tc(const PagedDims& pd, const PagedAttnArgs& a, void* ws, cudaStream_t st);
+
 // Lengths of request s as the kernels use them: rows [q0, q0 + ql) and kv
 // cached positions; ql = 0 and a report where they do not fit the call.
 struct SeqLen {

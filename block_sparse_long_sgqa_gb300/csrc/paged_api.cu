@@ -107,7 +107,8 @@ SGQA_API int sgqa_paged_append(const sgqa_paged_params* p, const void* K, const 
 SGQA_API size_t sgqa_paged_workspace_bytes(const sgqa_paged_params* p) {
   PagedDims pd;
   if (derive_paged(p, &pd) != SGQA_OK) return 0;
-  return paged_simt_ws_bytes(pd) + 256;  // slack to align the caller's base
+  return (pd.dtype == SGQA_BF16 ? paged_tc_ws_bytes(pd) : paged_simt_ws_bytes(pd)) +
+         256;  // slack to align the caller's base
 }
 
 SGQA_API int sgqa_paged_attn(const sgqa_paged_params* p, const void* Q, const void* K_pages,
@@ -127,7 +128,9 @@ SGQA_API int sgqa_paged_attn(const sgqa_paged_params* p, const void* Q, const vo
   void* base = reinterpret_cast<void*>((reinterpret_cast<uintptr_t>(ws) + 255) &
                                        ~static_cast<uintptr_t>(255));
   const PagedAttnArgs a{Q, K_pages, V_pages, page_table, q_start, kv_len, O, lse, status};
-  return launch_paged_simt(pd, a, base, reinterpret_cast<cudaStream_t>(stream));
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return pd.dtype == SGQA_BF16 ? launch_paged_tc(pd, a, base, st)
+                               : launch_paged_simt(pd, a, base, st);
 }
 
 }  // extern "C"

@@ -1,0 +1,912 @@
+// Ragged attention over the paged pool on tcgen05 tensor cores (bf16).
+//
+// Online softmax in one pass over a request's keys, 128 at a time: S = Q K^T
+// into tensor memory, P = 2^(S scale log2 e - m) rounded to bf16 (m: a running
+// reference maximum, raised only when a tile exceeds it by much), O += P V, and
+// at the end O / l with l the sum of P in fp32.
+//
+// A query tile is 128 / G tokens with their G query heads as the M = 128 rows of
+// every product, so each K and V tile that is read serves the whole KV group.
+// The work is cut into pieces (request, KV group, item of up to two query
+// tiles, chunk of its keys).  One CTA per SM walks pieces blockIdx.x, + grid,
+// ...: neighbouring pieces are the items of one (request, group, chunk), so
+// the CTAs running at one time read the same keys, from L2 after the first.
+// Requests with one query tile (single tokens, drafts) let the two softmax
+// groups take alternate key tiles; longer ones give each group its own query
+// tile, and each key tile serves both.
+//
+// Roles (12 warps): 0 walks the pieces, publishes them in a ring and loads Q;
+// 1 and 2 load K and V tiles through the page table (TMA boxes of gcd(page
+// size, 128) rows, one lane each); 3 issues the products; 4-7 and 8-11 are the
+// softmax groups, one thread per row, and write the outputs.  All rings run
+// on across pieces, so the next piece's keys load during the current one.
+#include "paged.h"
+
+namespace sgqa {
+namespace {
+
+constexpr unsigned FULL = 0xffffffffu;
+constexpr int BM = 128;   // rows of a query tile
+constexpr int KB = 128;   // keys of a tile
+constexpr int NPC = 4;    // pieces in the ring
+constexpr int NTHREADS = 384;
+constexpr int kGrid = 152;
+
+// The reference maximum may lag behind by this much in the sum of a tile's
+// weights before it is raised: bf16 and fp32 hold such weights with the same
+// relative precision as weights up to 1.
+constexpr float kLazySum = 4096.0f;
+
+template <int D>
+struct Cfg {
+  static constexpr int KC = D / 64;                    // 64-column halves
+  static constexpr int TILE = KC * BM * 128;           // bytes of a 128-row operand tile
+  static constexpr int SK = D == 128 ? 3 : 6, SV = D == 128 ? 2 : 5;
+  static constexpr int OFF_Q = 0;                      // two query tiles
+  static constexpr int OFF_K = OFF_Q + 2 * TILE;
+  static constexpr int OFF_V = OFF_K + SK * TILE;
+  static constexpr int OFF_X = OFF_V + SV * TILE;      // maxima and sums [2][2][BM] floats
+  static constexpr int OFF_PC = OFF_X + 4 * BM * 4;    // piece ring
+  static constexpr int OFF_BAR = OFF_PC + NPC * 64;
+  static constexpr int NBAR = 2 * NPC + 2 + 2 * SK + 2 * SV + 6 + 4;
+  static constexpr int SMEM = OFF_BAR + NBAR * 8 + 64;
+  static_assert(SMEM <= 232448, "shared memory of one CTA");
+};
+
+struct TcArgs {
+  PagedDims pd;
+  const int32_t *page_table, *q_start, *kv_len;
+  __nv_bfloat16* O;
+  float* lse;
+  float *opart, *lpart;  // partial outputs [slot][slot_rows][D], their lse [slot][slot_rows]
+  int32_t* items;        // split items [ ][8]; items[-4]: their number
+  int32_t* status;
+  int slot_rows;
+  int box;               // rows of a K/V box: gcd(page size, 128)
+  int tpm;               // tokens of a query tile
+  float sl2;             // scale * log2(e)
+};
+
+struct Piece {
+  int s, g, row0, ntok;  // request, KV group, first token row, tokens
+  int pos0;              // position of the first token
+  int tb, n;             // first key tile, key tiles
+  int lo, hi;            // keys that some row of the item sees
+  int single;            // one query tile, key tiles alternate between the groups
+  int slot;              // partial output (-1: the piece is the whole item)
+  int end;               // no further piece
+};
+static_assert(sizeof(Piece) <= 64, "ring slot");
+
+// How a request is cut, for chunks of C key tiles.
+struct Cut {
+  int ipt;      // tokens per item
+  int items;    // per KV group
+  int span;     // most key tiles of an item
+  int ns, cs;   // chunks of an item, key tiles of a chunk
+};
+__device__ __forceinline__ Cut cut_of(const PagedDims& pd, int tpm, const SeqLen& q, int C) {
+  Cut c;
+  c.ipt = q.ql <= tpm ? tpm : 2 * tpm;
+  c.items = (q.ql + c.ipt - 1) / c.ipt;
+  c.span = (q.kv + KB - 1) / KB;
+  if (pd.window > 0) {
+    const int64_t seen = (int64_t)pd.window + c.ipt - 1;
+    const int64_t w = (seen + KB - 1) / KB + 1;
+    if (w < c.span) c.span = (int)w;
+  }
+  c.ns = c.span > C ? (c.span + C - 1) / C : 1;
+  c.cs = (c.span + c.ns - 1) / c.ns;
+  return c;
+}
+
+// Sum of a over the block (every thread gets it); `buf` holds 12 values.
+__device__ long long block_sum(long long a, long long* buf) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(FULL, a, o);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = a;
+  __syncthreads();
+  long long t = 0;
+#pragma unroll
+  for (int i = 0; i < NTHREADS / 32; ++i) t += buf[i];
+  return t;
+}
+
+// Walks the pieces of one CTA: lanes hold 32 requests at a time.
+struct Walk {
+  int64_t p, base;       // next piece; pieces before the 32 requests
+  int64_t slots, items;  // partial outputs and split items before them
+  int s0;
+  SeqLen q;              // this lane's request
+  Cut c;
+  int64_t n, ns, ni;     // its pieces, partial outputs and split items
+  int64_t inc, sinc, iinc;  // inclusive sums over the lanes
+};
+
+__device__ __forceinline__ int64_t lane_scan(int64_t v) {
+  const int lane = lane_id();
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(FULL, v, o);
+    if (lane >= o) v += x;
+  }
+  return v;
+}
+
+__device__ __forceinline__ void walk_load(const TcArgs& a, Walk& w, int C) {
+  const int s = w.s0 + (int)lane_id();
+  w.q = SeqLen{0, 0, 0};
+  if (s < a.pd.N) w.q = seq_len_of(a.pd, a.q_start, a.kv_len, s, a.status, blockIdx.x == 0);
+  w.c = cut_of(a.pd, a.tpm, w.q, C);
+  w.n = (int64_t)a.pd.Hkv * w.c.items * w.c.ns;
+  w.ns = w.c.ns > 1 ? w.n : 0;
+  w.ni = w.c.ns > 1 ? (int64_t)a.pd.Hkv * w.c.items : 0;
+  w.inc = lane_scan(w.n);
+  w.sinc = lane_scan(w.ns);
+  w.iinc = lane_scan(w.ni);
+}
+
+// The next piece of this CTA (warp-wide; false: none left).
+__device__ bool walk_next(const TcArgs& a, Walk& w, int C, Piece& pc) {
+  for (;;) {
+    const int64_t total = __shfl_sync(FULL, w.inc, 31);
+    if (w.p < w.base + total) break;
+    w.base += total;
+    w.slots += __shfl_sync(FULL, w.sinc, 31);
+    w.items += __shfl_sync(FULL, w.iinc, 31);
+    w.s0 += 32;
+    if (w.s0 >= a.pd.N) return false;
+    walk_load(a, w, C);
+  }
+  const int l = __ffs(__ballot_sync(FULL, w.base + w.inc > w.p)) - 1;
+  const int q0 = __shfl_sync(FULL, w.q.q0, l), ql = __shfl_sync(FULL, w.q.ql, l);
+  const int kv = __shfl_sync(FULL, w.q.kv, l);
+  const int ipt = __shfl_sync(FULL, w.c.ipt, l), items = __shfl_sync(FULL, w.c.items, l);
+  const int ns = __shfl_sync(FULL, w.c.ns, l), cs = __shfl_sync(FULL, w.c.cs, l);
+  const int64_t first = w.base + __shfl_sync(FULL, w.inc - w.n, l);
+  const int64_t slot0 = w.slots + __shfl_sync(FULL, w.sinc - w.ns, l);
+  const int64_t item0 = w.items + __shfl_sync(FULL, w.iinc - w.ni, l);
+  const int64_t r = w.p - first;
+  const int it = items - 1 - (int)(r % items);  // the longest items first
+  const int64_t gj = r / items;
+  const int j = (int)(gj % ns);
+  pc.s = w.s0 + l;
+  pc.g = (int)(gj / ns);
+  pc.row0 = q0 + it * ipt;
+  pc.ntok = min(ipt, ql - it * ipt);
+  pc.pos0 = kv - ql + it * ipt;
+  pc.hi = a.pd.causal ? max(0, min(kv, pc.pos0 + pc.ntok)) : kv;
+  pc.lo = a.pd.window ? max(0, pc.pos0 + 1 - a.pd.window) : 0;
+  pc.tb = pc.lo / KB + j * cs;
+  const int te = min(pc.tb + cs, (pc.hi + KB - 1) / KB);
+  pc.n = pc.hi > pc.lo ? max(0, te - pc.tb) : 0;
+  pc.single = pc.ntok <= a.tpm;
+  pc.slot = ns > 1 ? (int)(slot0 + r) : -1;
+  pc.end = 0;
+  if (ns > 1 && j == 0 && lane_id() == 0) {  // for the merge
+    int4* rec = reinterpret_cast<int4*>(a.items) + 2 * (item0 + (int64_t)pc.g * items + it);
+    rec[0] = make_int4(pc.row0, pc.ntok, pc.g, pc.single);
+    rec[1] = make_int4(pc.slot, items, ns, 0);
+  }
+  w.p += gridDim.x;
+  return true;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Bounded wait that polls: for the hand-offs of the product pipeline, where a
+// suspended wait's wake-up costs more than the polling.
+__device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, const Abort& ab,
+                                          int32_t* status, int where) {
+  if (mbar_test(bar, parity)) return true;
+  const uint64_t t0 = globaltimer();
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_test(bar, parity)) return true;
+    if ((i & 255) == 0) {
+      if (ab.set()) return false;
+      if (globaltimer() - t0 > kWaitLimitNs) {
+        ab.raise(status, where);
+        return false;
+      }
+    }
+  }
+}
+
+// Bits of keys [k, k + 32) that lie in [lo, hi).
+__device__ __forceinline__ uint32_t seen_bits(int k, int lo, int hi) {
+  const int a = max(lo - k, 0), b = min(hi - k, 32);
+  if (b <= a) return 0u;
+  return (b >= 32 ? FULL : (1u << b) - 1u) & ~((1u << a) - 1u);
+}
+
+// A tile in two passes: its masked maximum, then the weights; raises the
+// reference maximum and rescales what was accumulated under the old one.
+// S (128 columns at tS) is overwritten by P.  Returns the maximum and the sum.
+template <int D>
+__device__ __noinline__ float2 tile_two_pass(uint32_t tS, uint32_t tO, float sl2, uint32_t a0,
+                                             uint32_t a1, uint32_t a2, uint32_t a3, bool have_o,
+                                             float m_used, float l) {
+  const float ninf = -__int_as_float(0x7f800000);
+  float mx = ninf;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t v[32];
+    tmem_ld32(tS + c * 32, v);
+    tmem_wait_ld();
+    const uint32_t am = c == 0 ? a0 : c == 1 ? a1 : c == 2 ? a2 : a3;
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      mx = fmaxf(mx, ((am >> e) & 1u) ? __uint_as_float(v[e]) : ninf);
+  }
+  const float smax = mx * sl2;
+  const bool raise = smax > m_used;
+  const float f = raise ? ex2(m_used - smax) : 1.0f;  // 0 for the first keys a row sees
+  if (have_o && __any_sync(FULL, raise)) {
+#pragma unroll 1
+    for (int c = 0; c < D / 32; ++c) {
+      uint32_t o[32];
+      tmem_ld32(tO + c * 32, o);
+      tmem_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+      tmem_st32(tO + c * 32, o);
+    }
+  }
+  l *= f;
+  if (raise) m_used = smax;
+  const float msub = m_used == ninf ? 0.0f : m_used;
+  float sum = 0.0f;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t v[32], pk[16];
+    tmem_ld32(tS + c * 32, v);
+    tmem_wait_ld();
+    const uint32_t am = c == 0 ? a0 : c == 1 ? a1 : c == 2 ? a2 : a3;
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+      const float p0 = ((am >> e) & 1u) ? ex2(fmaf(__uint_as_float(v[e]), sl2, -msub)) : 0.0f;
+      const float p1 =
+          ((am >> (e + 1)) & 1u) ? ex2(fmaf(__uint_as_float(v[e + 1]), sl2, -msub)) : 0.0f;
+      sum += p0 + p1;
+      pk[e >> 1] = pack_bf16x2(p0, p1);
+    }
+    tmem_st16(tS + c * 16, pk);  // over S values that have been read
+  }
+  return make_float2(m_used, l + sum);
+}
+
+template <int D>
+__global__ void __launch_bounds__(NTHREADS, 1)
+    k_paged_attn(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                 const __grid_constant__ CUtensorMap mv, const __grid_constant__ TcArgs a) {
+  using C = Cfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (smem_u32(smem) & 1023u) {  // the operand tiles' swizzle needs it
+    if (blockIdx.x == 0 && threadIdx.x == 0) report(a.status, SGQA_ERR_BOUNDS, 330);
+    return;
+  }
+  auto piece_at = [&](int i) -> Piece& {
+    return *reinterpret_cast<Piece*>(smem + C::OFF_PC + (i % NPC) * 64);
+  };
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* pc_full = bars;                 // [NPC]
+  uint64_t* pc_empty = pc_full + NPC;       // [NPC]
+  uint64_t* q_full = pc_empty + NPC;
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* k_full = q_empty + 1;           // [SK]
+  uint64_t* k_empty = k_full + C::SK;       // [SK]
+  uint64_t* v_full = k_empty + C::SK;       // [SV]
+  uint64_t* v_empty = v_full + C::SV;       // [SV]
+  uint64_t* s_full = v_empty + C::SV;       // [2] S of a group's key tile
+  uint64_t* p_full = s_full + 2;            // [2] its P
+  uint64_t* o_full = p_full + 2;            // [2] a group's last product of a piece done
+  uint64_t* x_bar = o_full + 2;             // [2] groups joined: statistics, outputs read
+  uint64_t* mma_done = x_bar + 2;
+  uint64_t* stall_bar = mma_done + 1;       // nothing arrives on it
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::NBAR);
+  int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+  float* xmax = reinterpret_cast<float*>(smem + C::OFF_X);  // [2][BM]
+  float* xsum = xmax + 2 * BM;                              // [2][BM]
+  const int warp = warp_id(), lane = lane_id();
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NPC; ++i) {
+      mbar_init(&pc_full[i], 1);
+      mbar_init(&pc_empty[i], 11);  // K, V, products, 8 softmax warps
+    }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    for (int i = 0; i < C::SK; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+    }
+    for (int i = 0; i < C::SV; ++i) {
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&o_full[i], 1);
+      mbar_init(&x_bar[i], 8);
+    }
+    mbar_init(mma_done, 1);
+    mbar_init(stall_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 3) tmem_alloc(tmem_slot, 512);
+
+  // ---- chunk size: the work in key tiles over the grid, the same in every CTA
+  int chunk;
+  {
+    long long* buf = reinterpret_cast<long long*>(xmax);
+    long long u = 0;
+    for (int s = threadIdx.x; s < a.pd.N; s += NTHREADS) {
+      const SeqLen q = seq_len_of(a.pd, a.q_start, a.kv_len, s, nullptr, false);
+      const Cut c = cut_of(a.pd, a.tpm, q, 0x7fffffff);
+      u += (long long)a.pd.Hkv * c.items * c.span;
+    }
+    u = block_sum(u, buf);
+    const long long want = (u + 2 * kGrid - 1) / (2 * kGrid);
+    chunk = (int)(want < 2 ? 2 : want > 0x3fffffff ? 0x3fffffff : want);
+    if (blockIdx.x == 0) {  // the merge reads how many items are split
+      long long ni = 0;
+      for (int s = threadIdx.x; s < a.pd.N; s += NTHREADS) {
+        const SeqLen q = seq_len_of(a.pd, a.q_start, a.kv_len, s, nullptr, false);
+        const Cut c = cut_of(a.pd, a.tpm, q, chunk);
+        ni += c.ns > 1 ? (long long)a.pd.Hkv * c.items : 0;
+      }
+      ni = block_sum(ni, buf);
+      if (threadIdx.x == 0) a.items[-4] = (int32_t)ni;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const Abort ab{abort_flag};
+
+  if (warp == 0) {
+    // ============================================================ pieces, Q
+    if (lane == 0) tma_prefetch_desc(&mq);
+    Walk w;
+    w.p = blockIdx.x;
+    w.base = w.slots = w.items = 0;
+    w.s0 = 0;
+    walk_load(a, w, chunk);
+    int pub = 0, nq = 0, loads = 0;  // pieces published, their Q looked after, Q loads issued
+    bool done = false;
+    uint64_t t_prog = globaltimer();
+    uint32_t idle = 0;
+    while (!done || nq < pub) {
+      bool progress = false;
+      if (!done && pub - nq < NPC &&
+          __shfl_sync(FULL, (int)mbar_test(&pc_empty[pub % NPC], (uint32_t)(((pub / NPC) & 1) ^ 1)),
+                      0)) {
+        Piece pc;
+        if (!walk_next(a, w, chunk, pc)) {
+          pc = Piece{};
+          pc.end = 1;
+          done = true;
+        }
+        if (lane == 0) {
+          piece_at(pub) = pc;
+          mbar_arrive(&pc_full[pub % NPC]);
+        }
+        __syncwarp();
+        ++pub;
+        progress = true;
+      }
+      if (nq < pub) {
+        const Piece& pc = piece_at(nq);
+        if (pc.n == 0) {
+          ++nq;
+          progress = true;
+        } else if (__shfl_sync(FULL, (int)mbar_test(q_empty, (uint32_t)((loads & 1) ^ 1)), 0)) {
+          if (lane == 0) {
+            const int tiles = pc.single ? 1 : 2;
+            mbar_expect_tx(q_full, (uint32_t)(tiles * C::KC * 128 * a.pd.G * a.tpm));
+            for (int i = 0; i < tiles; ++i)
+              for (int c = 0; c < C::KC; ++c)  // rows (token, head) of the box
+                tma_load_3d(smem + C::OFF_Q + i * C::TILE + c * (BM * 128), &mq, q_full, c * 64,
+                            pc.g * a.pd.G, pc.row0 + i * a.tpm);
+          }
+          __syncwarp();
+          ++loads;
+          ++nq;
+          progress = true;
+        }
+      }
+      if (progress) {
+        t_prog = globaltimer();
+        idle = 0;
+      } else {
+        __nanosleep(64);
+        if ((++idle & 63) == 0) {
+          int stop = 0;
+          if (lane == 0) {
+            if (ab.set()) {
+              stop = 1;
+            } else if (globaltimer() - t_prog > kWaitLimitNs) {
+              ab.raise(a.status, 331);
+              stop = 1;
+            }
+          }
+          if (__shfl_sync(FULL, stop, 0)) break;
+        }
+      }
+    }
+    if (lane == 0 && ab.set() && loads > 0)
+      mbar_wait_drain(q_full, (uint32_t)((loads - 1) & 1), a.status, 391);
+  } else if (warp <= 2) {
+    // ========================================================== K or V loads
+    const bool isK = warp == 1;
+    const CUtensorMap* map = isK ? &mk : &mv;
+    uint64_t* full = isK ? k_full : v_full;
+    uint64_t* empty = isK ? k_empty : v_empty;
+    const int NS = isK ? C::SK : C::SV;
+    uint8_t* slots = smem + (isK ? C::OFF_K : C::OFF_V);
+    if (lane == 0) tma_prefetch_desc(map);
+    const int rows_total = a.pd.n_pages * a.pd.Hkv * a.pd.ps;
+    const int nbox = KB / a.box;
+    int cnt = 0;  // tiles loaded
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
+      ok = __all_sync(FULL, mbar_wait(&pc_full[i % NPC], (uint32_t)((i / NPC) & 1), ab, a.status, 332));
+      if (!ok) break;
+      const Piece pc = piece_at(i);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&pc_empty[i % NPC]);
+      if (pc.end) break;
+      const int32_t* row = a.page_table + (int64_t)pc.s * a.pd.max_pages;
+      for (int t = 0; t < pc.n; ++t, ++cnt) {
+        // this lane's box: keys key .. key + box - 1, skipped when none is seen
+        const int key = (pc.tb + t) * KB + lane * a.box;
+        const bool on = lane < nbox && key < pc.hi && key + a.box > pc.lo;
+        int at = rows_total;  // outside the pool: zeros
+        if (on) {
+          const int pi = key / a.pd.ps, page = row[pi];
+          if (page >= 0 && page < a.pd.n_pages)
+            at = (page * a.pd.Hkv + pc.g) * a.pd.ps + (key - pi * a.pd.ps);
+          else
+            report(a.status, SGQA_ERR_BOUNDS, 302);
+        }
+        const int boxes = __popc(__ballot_sync(FULL, on));
+        const int sl = cnt % NS;
+        ok = __all_sync(FULL, mbar_wait(&empty[sl], (uint32_t)(((cnt / NS) & 1) ^ 1), ab, a.status,
+                                        isK ? 333 : 334));
+        if (!ok) break;
+        if (lane == 0) mbar_expect_tx(&full[sl], (uint32_t)(boxes * a.box * 128 * C::KC));
+        __syncwarp();
+        if (on)
+          for (int c = 0; c < C::KC; ++c)
+            tma_load_2d(slots + sl * C::TILE + c * (KB * 128) + lane * a.box * 128, map, &full[sl],
+                        c * 64, at);
+        __syncwarp();
+      }
+    }
+    if (lane == 0 && ab.set())  // copies in flight land before the CTA ends
+      for (int k = 0; k < NS; ++k) {
+        const int uses = cnt / NS + (k < cnt % NS ? 1 : 0);
+        if (uses > 0) mbar_wait_drain(&full[k], (uint32_t)((uses - 1) & 1), a.status, isK ? 392 : 393);
+      }
+  } else if (warp == 3) {
+    // ============================================================== products
+    if (lane == 0) {
+      constexpr uint32_t idesc_qk = idesc_bf16_f32(BM, KB, 0, 0);
+      constexpr uint32_t idesc_pv = idesc_bf16_f32(BM, D, 0, 1);
+      const uint32_t sQ = smem_u32(smem + C::OFF_Q), sK = smem_u32(smem + C::OFF_K);
+      const uint32_t sV = smem_u32(smem + C::OFF_V);
+      int kc = 0, vc = 0;           // key tiles consumed before this piece
+      int pcnt0 = 0, pcnt1 = 0;     // P tiles waited for, per group
+      int qn = 0;                   // pieces with products
+      bool ok = true;
+      for (int i = 0; ok; ++i) {
+        ok = mbar_wait(&pc_full[i % NPC], (uint32_t)((i / NPC) & 1), ab, a.status, 335);
+        if (!ok) break;
+        const Piece pc = piece_at(i);
+        if (pc.end || pc.n == 0) {
+          mbar_arrive(&pc_empty[i % NPC]);
+          if (pc.end) break;
+          continue;
+        }
+        ok = mbar_wait(q_full, (uint32_t)(qn & 1), ab, a.status, 336);
+        // Debug request (host-set status[3]): the first piece waits on a barrier
+        // nothing arrives on, so the pipeline gives up (detail 220) while its K
+        // and V copies are in flight.
+        if (ok && blockIdx.x == 0 && qn == 0 && debug_request(a.status) == SGQA_DEBUG_STALL)
+          ok = mbar_wait(stall_bar, 0, ab, a.status, 220, kDebugStallNs);
+        if (!ok) break;
+        ++qn;
+        mbar_arrive(&pc_empty[i % NPC]);
+        const int sh = pc.single ? 0 : 1;  // a key tile serves 1 << sh products of each kind
+        const int J = pc.n << sh;
+        // S of step j: group j & 1, key tile j >> sh, query tile j & sh
+        auto do_qk = [&](int j) -> bool {
+          const int t = kc + (j >> sh), ks = t % C::SK, grp = j & 1;
+          if (!mbar_poll(&k_full[ks], (uint32_t)((t / C::SK) & 1), ab, a.status, 337)) return false;
+          tc_fence_after();
+          const uint32_t q = sQ + (j & sh) * C::TILE, k = sK + ks * C::TILE;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * (BM * 128) + (kk & 3) * 32;
+            umma_f16(tmem + grp * 128, sdesc_sw128(q + off, 16, 1024), sdesc_sw128(k + off, 16, 1024),
+                     idesc_qk, kk > 0 ? 1u : 0u);
+          }
+          umma_commit(&s_full[grp]);
+          if ((j & sh) == sh) umma_commit(&k_empty[ks]);
+          if (j == J - 1) umma_commit(q_empty);
+          return true;
+        };
+        ok = do_qk(0) && (J < 2 || do_qk(1));
+        for (int j = 0; ok && j < J; ++j) {
+          const int t = vc + (j >> sh), vs = t % C::SV, grp = j & 1;
+          ok = mbar_poll(&v_full[vs], (uint32_t)((t / C::SV) & 1), ab, a.status, 338) &&
+               mbar_poll(&p_full[grp], (uint32_t)((grp ? pcnt1 : pcnt0) & 1), ab, a.status, 339);
+          if (!ok) break;
+          if (grp)
+            ++pcnt1;
+          else
+            ++pcnt0;
+          tc_fence_after();
+          const uint32_t v = sV + vs * C::TILE;
+#pragma unroll
+          for (int kk = 0; kk < KB / 16; ++kk)
+            umma_f16_ts(tmem + 256 + grp * 128, tmem + grp * 128 + kk * 8,
+                        sdesc_sw128(v + kk * 16 * 128, KB * 128, 1024), idesc_pv,
+                        (j > 1 || kk > 0) ? 1u : 0u);
+          if ((j & sh) == sh) umma_commit(&v_empty[vs]);
+          if (j + 2 >= J) umma_commit(&o_full[grp]);  // the group's last product
+          // products of one thread run in issue order, so this S overwrites P
+          // only after the product above has read it
+          if (j + 2 < J) ok = do_qk(j + 2);
+        }
+        kc += pc.n;
+        vc += pc.n;
+      }
+      umma_commit(mma_done);
+      mbar_wait_drain(mma_done, 0, a.status, 399);
+    }
+  } else {
+    // =============================================================== softmax
+    const int grp = (warp - 4) >> 2, quad = warp & 3;
+    const int r = quad * 32 + lane;
+    const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const uint32_t tS = tl + grp * 128, tO = tl + 256 + grp * 128;
+    const float ninf = -__int_as_float(0x7f800000);
+    const float sl2 = a.sl2;
+    const uint64_t sl2x2 = f2_pack(sl2, sl2);
+    const int G = a.pd.G, rt = r / G, rh = r - rt * G;  // token and head of the row in its tile
+    int sc = 0, oc = 0, xc = 0, vbase = 0;
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
+      ok = __all_sync(FULL, mbar_wait(&pc_full[i % NPC], (uint32_t)((i / NPC) & 1), ab, a.status, 340));
+      if (!ok) break;
+      const Piece pc = piece_at(i);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&pc_empty[i % NPC]);
+      if (pc.end) break;
+      const int tok = rt + (pc.single ? 0 : grp * a.tpm);
+      const bool row_ok = rt < a.tpm && tok < pc.ntok;
+      const bool active = __any_sync(FULL, row_ok);
+      const int pos = pc.pos0 + tok;
+      const int hi = !row_ok ? 0x7fffffff : a.pd.causal ? min(pc.hi, pos + 1) : pc.hi;
+      const int lo = !row_ok ? 0 : a.pd.window ? max(pc.lo, pos + 1 - a.pd.window) : pc.lo;
+      float m_used = ninf, l = 0.0f;
+      const int step = pc.single ? 2 : 1;
+      const int t0 = pc.single ? grp : 0;
+      for (int t = t0; t < pc.n; t += step) {
+        ok = __all_sync(FULL, mbar_poll(&s_full[grp], (uint32_t)(sc & 1), ab, a.status, 341));
+        if (!ok) break;
+        ++sc;
+        tc_fence_after();
+        const int k0 = (pc.tb + t) * KB;
+        if (active) {
+          const bool whole = __all_sync(FULL, lo <= k0 && k0 + KB <= hi);
+          bool fast = whole && __all_sync(FULL, m_used != ninf || !row_ok);
+          if (fast) {
+            // One pass under the reference maximum; P is written only if the
+            // tile's weights sum to at most kLazySum in every row.
+            const float nm = row_ok ? -m_used : ninf;
+            const uint64_t nm2 = f2_pack(nm, nm);
+            uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+            uint32_t pk[64];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t v[64];
+              tmem_ld32(tS + h * 64, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
+              tmem_ld32(tS + h * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 64; e += 2) {
+                float x0, x1;
+                f2_unpack(f2_fma(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sl2x2,
+                                 nm2), x0, x1);
+                const float p0 = ex2(x0), p1 = ex2(x1);
+                acc[(e >> 1) & 3] = f2_add(acc[(e >> 1) & 3], f2_pack(p0, p1));
+                pk[h * 32 + (e >> 1)] = pack_bf16x2(p0, p1);
+              }
+            }
+            float s0, s1;
+            f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), s0, s1);
+            const float sum = s0 + s1;
+            fast = __all_sync(FULL, sum <= kLazySum || !row_ok);
+            if (fast) {
+              tmem_st32(tS, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
+              tmem_st32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
+              l += sum;
+            }
+          }
+          if (!fast) {
+            const float2 ml = tile_two_pass<D>(
+                tS, tO, sl2, seen_bits(k0, lo, hi), seen_bits(k0 + 32, lo, hi),
+                seen_bits(k0 + 64, lo, hi), seen_bits(k0 + 96, lo, hi), t > t0, m_used, l);
+            m_used = ml.x;
+            l = ml.y;
+          }
+        }
+        // Rows of V that no row of the item sees are zeroed before the product:
+        // they may hold anything, and 0 times an infinity or NaN would count.
+        if ((pc.single || grp == 0) && (pc.lo > k0 || pc.hi < k0 + KB)) {
+          const int vt = vbase + t, vs = vt % C::SV;
+          ok = __all_sync(FULL, mbar_wait(&v_full[vs], (uint32_t)((vt / C::SV) & 1), ab, a.status, 342));
+          if (!ok) break;
+          if (k0 + r < pc.lo || k0 + r >= pc.hi) {
+            uint8_t* vr = smem + C::OFF_V + vs * C::TILE + r * 128;
+            for (int c = 0; c < C::KC; ++c)
+              for (int b = 0; b < 128; b += 16)
+                *reinterpret_cast<uint4*>(vr + c * (KB * 128) + b) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[grp]);
+      }
+      if (!ok) break;
+      vbase += pc.n;
+      // ---- outputs
+      const int n0 = pc.single ? (pc.n + 1) / 2 : pc.n, n1 = pc.single ? pc.n / 2 : pc.n;
+      if ((grp == 0 ? n0 : n1) > 0) {
+        ok = __all_sync(FULL, mbar_wait(&o_full[grp], (uint32_t)(oc & 1), ab, a.status, 343));
+        if (!ok) break;
+        ++oc;
+      }
+      // a single tile with a part in each accumulator: the groups exchange their
+      // maxima and sums and share out the columns; else the group that has the
+      // part writes all of it
+      const bool share = pc.single && n1 > 0;
+      float g0, g1, lt = l, mm = m_used;
+      if (share) {
+        xmax[grp * BM + r] = m_used;
+        xsum[grp * BM + r] = l;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&x_bar[0]);
+        ok = __all_sync(FULL, mbar_wait(&x_bar[0], (uint32_t)(xc & 1), ab, a.status, 345));
+        if (!ok) break;
+        const float m0 = xmax[r], m1 = xmax[BM + r];
+        mm = fmaxf(m0, m1);
+        g0 = m0 == ninf ? 0.0f : ex2(m0 - mm);
+        g1 = m1 == ninf ? 0.0f : ex2(m1 - mm);
+        lt = xsum[r] * g0 + xsum[BM + r] * g1;
+      } else {
+        g0 = grp == 0 ? 1.0f : 0.0f;
+        g1 = 1.0f - g0;
+      }
+      tc_fence_after();
+      const float inv = lt > 0.0f ? 1.0f / lt : 0.0f;
+      g0 *= inv;
+      g1 *= inv;
+      const float lse = lt > 0.0f ? (mm + __log2f(lt)) * 0.69314718055994531f : ninf;
+      const bool mine = share || !pc.single || grp == 0;
+      const int c0 = share ? grp * (D / 64) : 0, c1 = share ? c0 + D / 64 : D / 32;
+      const int64_t orow = (int64_t)(pc.row0 + tok) * a.pd.H + (int64_t)pc.g * G + rh;
+      const int64_t prow = (int64_t)pc.slot * a.slot_rows + (pc.single ? 0 : grp * BM) + r;
+      if (mine && active) {
+        const bool use0 = share || (grp == 0 && n0 > 0), use1 = share || (grp == 1 && n1 > 0);
+#pragma unroll 1
+        for (int c = c0; c < c1; ++c) {
+          uint32_t o0[32], o1[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o0[e] = o1[e] = 0u;
+          if (use0) tmem_ld32(tl + 256 + c * 32, o0);
+          if (use1) tmem_ld32(tl + 384 + c * 32, o1);
+          tmem_wait_ld();
+          float ov[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            ov[e] = (use0 && g0 > 0.0f ? __uint_as_float(o0[e]) * g0 : 0.0f) +
+                    (use1 && g1 > 0.0f ? __uint_as_float(o1[e]) * g1 : 0.0f);
+          if (row_ok && pc.slot >= 0) {
+            float* dst = a.opart + prow * D + c * 32;
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<float4*>(dst + e) = make_float4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
+          } else if (row_ok) {
+            __nv_bfloat16* dst = a.O + orow * D + c * 32;
+#pragma unroll
+            for (int e = 0; e < 32; e += 8)
+              *reinterpret_cast<uint4*>(dst + e) =
+                  make_uint4(pack_bf16x2(ov[e], ov[e + 1]), pack_bf16x2(ov[e + 2], ov[e + 3]),
+                             pack_bf16x2(ov[e + 4], ov[e + 5]), pack_bf16x2(ov[e + 6], ov[e + 7]));
+          }
+          __syncwarp();  // the loads from tensor memory are warp-wide
+        }
+        if (row_ok && (grp == 0 || !pc.single)) {
+          if (pc.slot >= 0)
+            a.lpart[prow] = lse;
+          else
+            a.lse[(int64_t)(pc.g * G + rh) * a.pd.T + pc.row0 + tok] = lse;
+        }
+      }
+      if (share) {  // both groups have read both accumulators and the statistics
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&x_bar[1]);
+        ok = __all_sync(FULL, mbar_wait(&x_bar[1], (uint32_t)(xc & 1), ab, a.status, 346));
+        ++xc;
+      }
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == 3) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Merge of the split items' partial outputs in chunk order: lse = ln sum e^(lse_j),
+// O = sum e^(lse_j - lse) O_j.  A warp per row; a CTA takes 8 rows of an item.
+template <int D>
+__global__ void __launch_bounds__(256) k_paged_merge(const __grid_constant__ TcArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int n_items = a.items[-4];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int blocks = (a.slot_rows + 7) / 8;
+  const float ninf = -__int_as_float(0x7f800000);
+  for (int64_t u = blockIdx.x; u < (int64_t)n_items * blocks; u += gridDim.x) {
+    const int4* rec = reinterpret_cast<const int4*>(a.items) + 2 * (u / blocks);
+    const int4 r0 = rec[0], r1 = rec[1];
+    const int row = (int)(u % blocks) * 8 + warp;
+    if (row >= r0.y * a.pd.G) continue;
+    const int tok = row / a.pd.G, h = row - tok * a.pd.G;
+    const int tile = tok / a.tpm;  // rows of the second query tile start at BM
+    const int64_t at = (int64_t)r1.x * a.slot_rows + tile * BM + (tok - tile * a.tpm) * a.pd.G + h;
+    const int64_t stride = (int64_t)r1.y * a.slot_rows;
+    float mx = ninf;
+    for (int j = lane; j < r1.z; j += 32) mx = fmaxf(mx, a.lpart[at + j * stride]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, o));
+    float acc[D / 32], sw = 0.0f;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) acc[e] = 0.0f;
+    for (int j = 0; j < r1.z; ++j) {
+      const float lj = a.lpart[at + j * stride];
+      if (lj == ninf) continue;  // nothing seen in this chunk
+      const float w = expf(lj - mx);
+      sw += w;
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e)
+        acc[e] = fmaf(w, a.opart[(at + j * stride) * D + lane * (D / 32) + e], acc[e]);
+    }
+    const float inv = sw > 0.0f ? 1.0f / sw : 0.0f;
+    const int64_t t = r0.x + tok;
+    const int64_t hq = (int64_t)r0.z * a.pd.G + h;
+    __nv_bfloat16* dst = a.O + (t * a.pd.H + hq) * D + lane * (D / 32);
+#pragma unroll
+    for (int e = 0; e < D / 32; e += 2)
+      *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+    if (lane == 0) a.lse[hq * a.pd.T + t] = sw > 0.0f ? mx + logf(sw) : ninf;
+  }
+}
+
+// Most partial outputs of a call: a split item of n key tiles has fewer than 2 n /
+// chunk chunks, and chunk is at least 1 / (2 kGrid) of all tiles.
+constexpr int kSlots = 2 * 2 * kGrid;
+
+int slot_rows(const PagedDims& pd) {
+  const int64_t rows = (int64_t)pd.T * pd.G;
+  return (int)(rows < BM ? rows : 2 * BM);
+}
+
+struct Ws {
+  size_t items, lpart, opart, bytes;
+};
+Ws carve(const PagedDims& pd) {
+  Ws w;
+  const size_t rows = (size_t)kSlots * slot_rows(pd);
+  w.items = 256;  // the number of items stands before them
+  w.lpart = w.items + (((size_t)kSlots * 32 + 255) & ~size_t(255));
+  w.opart = w.lpart + ((rows * 4 + 255) & ~size_t(255));
+  w.bytes = w.opart + rows * pd.d * 4;
+  return w;
+}
+
+// Q [T][H][d] with row stride qs, boxes of one query tile's heads and tokens.
+bool q_map(const PagedDims& pd, int tpm, const void* Q, CUtensorMap* m) {
+  auto fn = tmap_encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)pd.d, (cuuint64_t)pd.H, (cuuint64_t)pd.T};
+  cuuint64_t str[2] = {(cuuint64_t)pd.d * 2, (cuuint64_t)pd.qs * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)pd.G, (cuuint32_t)tpm}, es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(Q), dims, str, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+int launch(const TcArgs& a, const PagedAttnArgs& pa, cudaStream_t st) {
+  using C = Cfg<D>;
+  const PagedDims& pd = a.pd;
+  CUtensorMap mq, mk, mv;
+  const uint64_t rows = (uint64_t)pd.n_pages * pd.Hkv * pd.ps;
+  if (!q_map(pd, a.tpm, pa.Q, &mq) ||
+      !make_tmap_2d_bf16(&mk, pa.K, D, rows, D * 2, 64, (uint32_t)a.box) ||
+      !make_tmap_2d_bf16(&mv, pa.V, D, rows, D * 2, 64, (uint32_t)a.box))
+    return SGQA_ERR_CUDA;
+  if (cudaFuncSetAttribute(k_paged_attn<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
+      cudaSuccess)
+    return SGQA_ERR_CUDA;
+  log_begin(SGQA_K_PAGED_ATTN, st);
+  k_paged_attn<D><<<kGrid, NTHREADS, C::SMEM, st>>>(mq, mk, mv, a);
+  log_end(st);
+  if (cudaGetLastError() != cudaSuccess) return SGQA_ERR_CUDA;
+  // the merge is scheduled while the attention drains and waits for its end
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * kGrid);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  log_begin(SGQA_K_PAGED_ATTN, st);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k_paged_merge<D>, a);
+  log_end(st);
+  return e == cudaSuccess ? SGQA_OK : SGQA_ERR_CUDA;
+}
+
+}  // namespace
+
+size_t paged_tc_ws_bytes(const PagedDims& pd) {
+  return pd.N == 0 || pd.T == 0 ? 0 : carve(pd).bytes;
+}
+
+int launch_paged_tc(const PagedDims& pd, const PagedAttnArgs& pa, void* ws, cudaStream_t st) {
+  const Ws w = carve(pd);
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  TcArgs a;
+  a.pd = pd;
+  a.page_table = pa.page_table;
+  a.q_start = pa.q_start;
+  a.kv_len = pa.kv_len;
+  a.O = static_cast<__nv_bfloat16*>(pa.O);
+  a.lse = pa.lse;
+  a.items = reinterpret_cast<int32_t*>(base + w.items);
+  a.lpart = reinterpret_cast<float*>(base + w.lpart);
+  a.opart = reinterpret_cast<float*>(base + w.opart);
+  a.status = pa.status;
+  a.slot_rows = slot_rows(pd);
+  int x = pd.ps, y = KB;
+  while (y) {
+    const int t = x % y;
+    x = y;
+    y = t;
+  }
+  a.box = x;
+  a.tpm = BM / pd.G;
+  a.sl2 = pd.scale * 1.4426950408889634f;
+  return pd.d == 128 ? launch<128>(a, pa, st) : launch<64>(a, pa, st);
+}
+
+}  // namespace sgqa
