@@ -323,39 +323,46 @@ def paged_pool(p: PagedParams, device="cuda"):
 
 
 _TORCH_DTYPE = {BF16: torch.bfloat16, FP32: torch.float32}
+_raw_stream = torch._C._cuda_getCurrentRawStream  # torch.cuda.current_stream() costs 3 us a call
 
 
 def _at(t, dtype, numel, dev, what):
-    """Device address of a contiguous tensor of at least `numel` values of `dtype`."""
-    if t.dtype != dtype or t.device != dev or not t.is_contiguous() or t.numel() < numel:
+    """Device address of a contiguous tensor of at least `numel` values of `dtype`
+    on device number `dev` (-1: the CPU)."""
+    if t.dtype != dtype or t.get_device() != dev or not t.is_contiguous() or t.numel() < numel:
         raise ValueError(f"{what}: expected a contiguous {dtype} tensor of at least {numel} "
-                         f"values on {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+                         f"values on device {dev}, got {t.dtype} {tuple(t.shape)} on "
+                         f"{t.device}")
     return t.data_ptr()
 
 
 def _rows_at(t, p, heads, stride, dev, what):
     """Device address of token rows [T][heads][d], packed but for the row stride."""
-    d = p.head_dim
-    if (t.dim() != 3 or t.dtype != _TORCH_DTYPE.get(p.dtype) or t.device != dev or
-            t.shape[0] < p.max_tokens or t.shape[1] != heads or t.shape[2] != d):
+    d, shape, strides = p.head_dim, t.shape, t.stride()
+    if (len(shape) != 3 or t.dtype != _TORCH_DTYPE.get(p.dtype) or t.get_device() != dev or
+            shape[0] < p.max_tokens or shape[1] != heads or shape[2] != d):
         raise ValueError(f"{what}: expected [{p.max_tokens}][{heads}][{d}] in the params' dtype "
-                         f"on {dev}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+                         f"on device {dev}, got {t.dtype} {tuple(shape)} on {t.device}")
     want = stride or heads * d
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d) or (
-            t.shape[0] > 1 and t.stride(0) != want):
-        raise ValueError(f"{what}: strides {t.stride()} are not ({want}, {d}, 1) of the params")
+    if strides[2] != 1 or (heads > 1 and strides[1] != d) or (
+            shape[0] > 1 and strides[0] != want):
+        raise ValueError(f"{what}: strides {strides} are not ({want}, {d}, 1) of the params")
     return t.data_ptr()
 
 
 def _paged_call(fn, what, dev, stream, *args):
-    """The call on `dev`: its current stream unless one is given, and that
-    device current while the library launches."""
-    if dev.type != "cuda":
+    """The call on device `dev`: on its current stream unless one is given, and
+    with that device current while the library launches."""
+    if dev < 0:
         raise ValueError(f"{what}: expected CUDA tensors")
-    if dev.index != torch.cuda.current_device():
+    st = _raw_stream(dev) if stream is None else _stream(stream)
+    if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
-            return _check(fn(*args, _stream(stream)), what)
-    _check(fn(*args, _stream(stream)), what)
+            rc = fn(*args, st)
+    else:
+        rc = fn(*args, st)
+    if rc != OK:
+        raise SgqaError(rc, what)
 
 
 def _status_at(status, dev):
@@ -365,7 +372,7 @@ def _status_at(status, dev):
 def sgqa_page_plan(p, q_len, kv_len, free_pages, n_free, page_table, q_start, slot_map, positions,
                    n_free_out, status=None, stream=None):
     """Page table rows, q_start, slot_map and positions of a step from its lengths."""
-    dev, i32, n = kv_len.device, torch.int32, p.n_seqs
+    dev, i32, n = kv_len.get_device(), torch.int32, p.n_seqs
     _paged_call(_lib.sgqa_page_plan, "sgqa_page_plan", dev, stream, ctypes.byref(p),
                 _at(q_len, i32, n, dev, "q_len"), _at(kv_len, i32, n, dev, "kv_len"),
                 _at(free_pages, i32, p.n_pages, dev, "free_pages"),
@@ -380,7 +387,7 @@ def sgqa_page_plan(p, q_len, kv_len, free_pages, n_free, page_table, q_start, sl
 def sgqa_page_release(p, kv_len, keep_len, page_table, free_pages, n_free, n_free_out,
                       status=None, stream=None):
     """Pages past each request's keep_len pushed back on the free stack."""
-    dev, i32, n = kv_len.device, torch.int32, p.n_seqs
+    dev, i32, n = kv_len.get_device(), torch.int32, p.n_seqs
     _paged_call(_lib.sgqa_page_release, "sgqa_page_release", dev, stream, ctypes.byref(p),
                 _at(kv_len, i32, n, dev, "kv_len"), _at(keep_len, i32, n, dev, "keep_len"),
                 _at(page_table, i32, n * p.max_pages, dev, "page_table"),
@@ -396,7 +403,7 @@ def _pool_at(t, p, dev, what):
 
 def sgqa_paged_append(p, K, V, slot_map, K_pages, V_pages, status=None, stream=None):
     """New K and V rows [T][Hkv][d] (row stride p.kv_stride) into the pool."""
-    dev = K_pages.device
+    dev = K_pages.get_device()
     _paged_call(_lib.sgqa_paged_append, "sgqa_paged_append", dev, stream, ctypes.byref(p),
                 _rows_at(K, p, p.n_kv_heads, p.kv_stride, dev, "K"),
                 _rows_at(V, p, p.n_kv_heads, p.kv_stride, dev, "V"),
@@ -408,7 +415,7 @@ def sgqa_paged_append(p, K, V, slot_map, K_pages, V_pages, status=None, stream=N
 def sgqa_paged_attn(p, Q, K_pages, V_pages, page_table, q_start, kv_len, O, lse, ws, status=None,
                     stream=None):
     """Attention of the step's tokens [T][H][d] over the paged pool: O and lse."""
-    dev, i32, n = K_pages.device, torch.int32, p.n_seqs
+    dev, i32, n = K_pages.get_device(), torch.int32, p.n_seqs
     _paged_call(_lib.sgqa_paged_attn, "sgqa_paged_attn", dev, stream, ctypes.byref(p),
                 _rows_at(Q, p, p.n_q_heads, p.q_stride, dev, "Q"),
                 _pool_at(K_pages, p, dev, "K_pages"), _pool_at(V_pages, p, dev, "V_pages"),
