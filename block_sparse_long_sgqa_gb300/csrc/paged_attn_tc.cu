@@ -7,19 +7,26 @@
 //
 // A query tile is 128 / G tokens with their G query heads as the M = 128 rows of
 // every product, so each K and V tile that is read serves the whole KV group.
-// The work is cut into pieces (request, KV group, item of up to two query
-// tiles, chunk of its keys).  One CTA per SM walks pieces blockIdx.x, + grid,
-// ...: neighbouring pieces are the items of one (request, group, chunk), so
-// the CTAs running at one time read the same keys, from L2 after the first.
+// An item is up to two query tiles of a (request, KV group); one CTA per SM.
 // Requests with one query tile (single tokens, drafts) let the two softmax
 // groups take alternate key tiles; longer ones give each group its own query
 // tile, and each key tile serves both.
 //
-// Roles (12 warps): 0 walks the pieces, publishes them in a ring and loads Q;
-// 1 and 2 load K and V tiles through the page table (TMA boxes of gcd(page
-// size, 128) rows, one lane each); 3 issues the products; 4-7 and 8-11 are the
-// softmax groups, one thread per row, and write the outputs.  All rings run
-// on across pieces, so the next piece's keys load during the current one.
+// Who does what follows from the lengths alone.  All items lie one after
+// another on a line, each as long as its work; the line is cut into one equal
+// range per CTA, and a key tile belongs to the CTA whose range holds its place.
+// An item cut by a range's end leaves partial outputs, which a second kernel
+// merges in order.  That balances any mix of lengths to a tile, but the CTAs
+// then read different keys at any one time.  When the keys that several items
+// share exceed what L2 holds, full waves of whole items come first: item w
+// grid + c goes to CTA c, so that neighbours read the same keys together, and
+// only the rest of each request's items goes on the line.
+//
+// Roles (12 warps): 0 walks this CTA's pieces, publishes them in a ring and
+// loads Q; 1 and 2 load K and V tiles through the page table (TMA boxes of
+// gcd(page size, 128) rows, one lane each); 3 issues the products; 4-7 and 8-11
+// are the softmax groups, one thread per row, and write the outputs.  All rings
+// run on across pieces, so the next piece's keys load during the current one.
 #include "paged.h"
 
 namespace sgqa {
@@ -48,7 +55,7 @@ struct Cfg {
   static constexpr int OFF_X = OFF_V + SV * TILE;      // maxima and sums [2][2][BM] floats
   static constexpr int OFF_PC = OFF_X + 4 * BM * 4;    // piece ring
   static constexpr int OFF_BAR = OFF_PC + NPC * 64;
-  static constexpr int NBAR = 2 * NPC + 2 + 2 * SK + 2 * SV + 6 + 4;
+  static constexpr int NBAR = 2 * NPC + 4 + 2 * SK + 2 * SV + 6 + 4;
   static constexpr int SMEM = OFF_BAR + NBAR * 8 + 64;
   static_assert(SMEM <= 232448, "shared memory of one CTA");
 };
@@ -59,11 +66,12 @@ struct TcArgs {
   __nv_bfloat16* O;
   float* lse;
   float *opart, *lpart;  // partial outputs [slot][slot_rows][D], their lse [slot][slot_rows]
-  int32_t* items;        // split items [ ][8]; items[-4]: their number
+  int4* rec;             // [kGrid][2]: the item that CTA c begins and another ends
   int32_t* status;
   int slot_rows;
   int box;               // rows of a K/V box: gcd(page size, 128)
   int tpm;               // tokens of a query tile
+  int wide;              // O is 32-byte aligned
   float sl2;             // scale * log2(e)
 };
 
@@ -78,119 +86,82 @@ struct Piece {
 };
 static_assert(sizeof(Piece) <= 64, "ring slot");
 
-// How a request is cut, for chunks of C key tiles.
+// Lengths on the line, in keys times a weight: a key tile takes kWt[..] * 128
+// (two query tiles cost about half as much again as one), an item kOver tiles
+// more for its beginning and end.  kOver >= 2 also keeps every tile's place
+// inside its item (an item's first and last tile may reach past its keys).
+constexpr int kWtSingle = 2, kWtDouble = 3;
+constexpr int kOver = 3;
+// Shortest range of a CTA, in line units: two key tiles of a single query tile.
+constexpr int64_t kLeastShare = 2 * KB * kWtSingle;
+// K and V bytes of the requests with several items above which waves are used:
+// about half of L2.
+constexpr int64_t kWaveBytes = int64_t(64) << 20;
+
+// How a request is cut: items per KV group, item k taking A + B k on the line.
 struct Cut {
-  int ipt;      // tokens per item
-  int items;    // per KV group
-  int span;     // most key tiles of an item
-  int ns, cs;   // chunks of an item, key tiles of a chunk
+  int q0, ql, kv;
+  int ipt, items;
+  int tw;               // a key tile on the line
+  int64_t A, B, head;   // head: all items of a KV group
 };
-__device__ __forceinline__ Cut cut_of(const PagedDims& pd, int tpm, const SeqLen& q, int C) {
-  Cut c;
-  c.ipt = q.ql <= tpm ? tpm : 2 * tpm;
-  c.items = (q.ql + c.ipt - 1) / c.ipt;
-  c.span = (q.kv + KB - 1) / KB;
-  if (pd.window > 0) {
-    const int64_t seen = (int64_t)pd.window + c.ipt - 1;
-    const int64_t w = (seen + KB - 1) / KB + 1;
-    if (w < c.span) c.span = (int)w;
+__device__ __forceinline__ Cut cut_of(const TcArgs& a, int s, bool tell) {
+  Cut c{0, 0, 0, 1, 0, 0, 0, 0, 0};
+  if (s >= a.pd.N) return c;
+  const SeqLen q = seq_len_of(a.pd, a.q_start, a.kv_len, s, a.status, tell);
+  c.q0 = q.q0;
+  c.ql = q.ql;
+  c.kv = q.kv;
+  const bool one = q.ql <= a.tpm;
+  const int wt = one ? kWtSingle : kWtDouble;
+  c.ipt = one ? a.tpm : 2 * a.tpm;
+  c.items = one ? (q.ql > 0) : (int)((unsigned)(q.ql + c.ipt - 1) / (unsigned)c.ipt);
+  c.tw = wt * KB;
+  // keys an item sees, at most
+  int keys = q.kv, slope = 0;
+  if (a.pd.window > 0) {
+    keys = min(q.kv, a.pd.window + c.ipt - 1);
+  } else if (a.pd.causal && q.kv >= q.ql) {
+    keys = q.kv - q.ql + c.ipt;
+    slope = c.ipt;
   }
-  c.ns = c.span > C ? (c.span + C - 1) / C : 1;
-  c.cs = (c.span + c.ns - 1) / c.ns;
+  c.A = (int64_t)(keys + kOver * KB) * wt;
+  c.B = (int64_t)slope * wt;
+  c.head = c.A * c.items + c.B * ((int64_t)c.items * (c.items - 1) / 2);
   return c;
 }
-
-// Sum of a over the block (every thread gets it); `buf` holds 12 values.
-__device__ long long block_sum(long long a, long long* buf) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(FULL, a, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = a;
-  __syncthreads();
-  long long t = 0;
-#pragma unroll
-  for (int i = 0; i < NTHREADS / 32; ++i) t += buf[i];
-  return t;
+// Where item k of a KV group begins, from the group's beginning.
+__device__ __forceinline__ int64_t item_at(int64_t A, int64_t B, int k) {
+  return A * k + B * ((int64_t)k * (k - 1) / 2);
 }
 
-// Walks the pieces of one CTA: lanes hold 32 requests at a time.
-struct Walk {
-  int64_t p, base;       // next piece; pieces before the 32 requests
-  int64_t slots, items;  // partial outputs and split items before them
-  int s0;
-  SeqLen q;              // this lane's request
-  Cut c;
-  int64_t n, ns, ni;     // its pieces, partial outputs and split items
-  int64_t inc, sinc, iinc;  // inclusive sums over the lanes
-};
+// Item k of group g of request s as one piece (warp-uniform arguments).
+__device__ __forceinline__ Piece item_piece(const TcArgs& a, int s, int q0, int ql, int kv, int ipt,
+                                            int g, int k) {
+  Piece pc;
+  pc.s = s;
+  pc.g = g;
+  pc.row0 = q0 + k * ipt;
+  pc.ntok = min(ipt, ql - k * ipt);
+  pc.pos0 = kv - ql + k * ipt;
+  pc.hi = a.pd.causal ? max(0, min(kv, pc.pos0 + pc.ntok)) : kv;
+  pc.lo = a.pd.window ? max(0, pc.pos0 + 1 - a.pd.window) : 0;
+  pc.tb = pc.lo / KB;
+  pc.n = pc.hi > pc.lo ? (pc.hi + KB - 1) / KB - pc.tb : 0;
+  pc.single = pc.ntok <= a.tpm;
+  pc.slot = -1;
+  pc.end = 0;
+  return pc;
+}
 
 __device__ __forceinline__ int64_t lane_scan(int64_t v) {
   const int lane = lane_id();
-#pragma unroll
+#pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t x = __shfl_up_sync(FULL, v, o);
     if (lane >= o) v += x;
   }
   return v;
-}
-
-__device__ __forceinline__ void walk_load(const TcArgs& a, Walk& w, int C) {
-  const int s = w.s0 + (int)lane_id();
-  w.q = SeqLen{0, 0, 0};
-  if (s < a.pd.N) w.q = seq_len_of(a.pd, a.q_start, a.kv_len, s, a.status, blockIdx.x == 0);
-  w.c = cut_of(a.pd, a.tpm, w.q, C);
-  w.n = (int64_t)a.pd.Hkv * w.c.items * w.c.ns;
-  w.ns = w.c.ns > 1 ? w.n : 0;
-  w.ni = w.c.ns > 1 ? (int64_t)a.pd.Hkv * w.c.items : 0;
-  w.inc = lane_scan(w.n);
-  w.sinc = lane_scan(w.ns);
-  w.iinc = lane_scan(w.ni);
-}
-
-// The next piece of this CTA (warp-wide; false: none left).
-__device__ bool walk_next(const TcArgs& a, Walk& w, int C, Piece& pc) {
-  for (;;) {
-    const int64_t total = __shfl_sync(FULL, w.inc, 31);
-    if (w.p < w.base + total) break;
-    w.base += total;
-    w.slots += __shfl_sync(FULL, w.sinc, 31);
-    w.items += __shfl_sync(FULL, w.iinc, 31);
-    w.s0 += 32;
-    if (w.s0 >= a.pd.N) return false;
-    walk_load(a, w, C);
-  }
-  const int l = __ffs(__ballot_sync(FULL, w.base + w.inc > w.p)) - 1;
-  const int q0 = __shfl_sync(FULL, w.q.q0, l), ql = __shfl_sync(FULL, w.q.ql, l);
-  const int kv = __shfl_sync(FULL, w.q.kv, l);
-  const int ipt = __shfl_sync(FULL, w.c.ipt, l), items = __shfl_sync(FULL, w.c.items, l);
-  const int ns = __shfl_sync(FULL, w.c.ns, l), cs = __shfl_sync(FULL, w.c.cs, l);
-  const int64_t first = w.base + __shfl_sync(FULL, w.inc - w.n, l);
-  const int64_t slot0 = w.slots + __shfl_sync(FULL, w.sinc - w.ns, l);
-  const int64_t item0 = w.items + __shfl_sync(FULL, w.iinc - w.ni, l);
-  const int64_t r = w.p - first;
-  const int it = items - 1 - (int)(r % items);  // the longest items first
-  const int64_t gj = r / items;
-  const int j = (int)(gj % ns);
-  pc.s = w.s0 + l;
-  pc.g = (int)(gj / ns);
-  pc.row0 = q0 + it * ipt;
-  pc.ntok = min(ipt, ql - it * ipt);
-  pc.pos0 = kv - ql + it * ipt;
-  pc.hi = a.pd.causal ? max(0, min(kv, pc.pos0 + pc.ntok)) : kv;
-  pc.lo = a.pd.window ? max(0, pc.pos0 + 1 - a.pd.window) : 0;
-  pc.tb = pc.lo / KB + j * cs;
-  const int te = min(pc.tb + cs, (pc.hi + KB - 1) / KB);
-  pc.n = pc.hi > pc.lo ? max(0, te - pc.tb) : 0;
-  pc.single = pc.ntok <= a.tpm;
-  pc.slot = ns > 1 ? (int)(slot0 + r) : -1;
-  pc.end = 0;
-  if (ns > 1 && j == 0 && lane_id() == 0) {  // for the merge
-    int4* rec = reinterpret_cast<int4*>(a.items) + 2 * (item0 + (int64_t)pc.g * items + it);
-    rec[0] = make_int4(pc.row0, pc.ntok, pc.g, pc.single);
-    rec[1] = make_int4(pc.slot, items, ns, 0);
-  }
-  w.p += gridDim.x;
-  return true;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -272,18 +243,21 @@ __device__ __noinline__ float2 tile_two_pass(uint32_t tS, uint32_t tO, float sl2
                                              uint32_t a1, uint32_t a2, uint32_t a3, bool have_o,
                                              float m_used, float l) {
   const float ninf = -__int_as_float(0x7f800000);
-  float mx = ninf;
+  float mx[4] = {ninf, ninf, ninf, ninf};
+  uint32_t v[64];
 #pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
-    uint32_t v[32];
-    tmem_ld32(tS + c * 32, v);
+  for (int h = 0; h < 2; ++h) {
+    tmem_ld32(tS + h * 64, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
+    tmem_ld32(tS + h * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
     tmem_wait_ld();
-    const uint32_t am = c == 0 ? a0 : c == 1 ? a1 : c == 2 ? a2 : a3;
+    const uint32_t am0 = h == 0 ? a0 : a2, am1 = h == 0 ? a1 : a3;
 #pragma unroll
-    for (int e = 0; e < 32; ++e)
-      mx = fmaxf(mx, ((am >> e) & 1u) ? __uint_as_float(v[e]) : ninf);
+    for (int e = 0; e < 32; ++e) {
+      mx[e & 1] = fmaxf(mx[e & 1], ((am0 >> e) & 1u) ? __uint_as_float(v[e]) : ninf);
+      mx[2 + (e & 1)] = fmaxf(mx[2 + (e & 1)], ((am1 >> e) & 1u) ? __uint_as_float(v[32 + e]) : ninf);
+    }
   }
-  const float smax = mx * sl2;
+  const float smax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
   const bool raise = smax > m_used;
   const float f = raise ? ex2(m_used - smax) : 1.0f;  // 0 for the first keys a row sees
   if (have_o && __any_sync(FULL, raise)) {
@@ -300,24 +274,41 @@ __device__ __noinline__ float2 tile_two_pass(uint32_t tS, uint32_t tO, float sl2
   l *= f;
   if (raise) m_used = smax;
   const float msub = m_used == ninf ? 0.0f : m_used;
-  float sum = 0.0f;
+  float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
-    uint32_t v[32], pk[16];
-    tmem_ld32(tS + c * 32, v);
+  for (int h = 0; h < 2; ++h) {
+    uint32_t pk[32];
+    tmem_ld32(tS + h * 64, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
+    tmem_ld32(tS + h * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
     tmem_wait_ld();
-    const uint32_t am = c == 0 ? a0 : c == 1 ? a1 : c == 2 ? a2 : a3;
+    const uint32_t am0 = h == 0 ? a0 : a2, am1 = h == 0 ? a1 : a3;
 #pragma unroll
-    for (int e = 0; e < 32; e += 2) {
-      const float p0 = ((am >> e) & 1u) ? ex2(fmaf(__uint_as_float(v[e]), sl2, -msub)) : 0.0f;
-      const float p1 =
-          ((am >> (e + 1)) & 1u) ? ex2(fmaf(__uint_as_float(v[e + 1]), sl2, -msub)) : 0.0f;
-      sum += p0 + p1;
+    for (int e = 0; e < 64; e += 2) {
+      const uint32_t am = e < 32 ? am0 : am1;
+      const float x0 = fmaf(__uint_as_float(v[e]), sl2, -msub);
+      const float x1 = fmaf(__uint_as_float(v[e + 1]), sl2, -msub);
+      const float p0 = ex2(((am >> (e & 31)) & 1u) ? x0 : ninf);
+      const float p1 = ex2(((am >> ((e & 31) + 1)) & 1u) ? x1 : ninf);
+      sum[e & 2] += p0;
+      sum[(e & 2) + 1] += p1;
       pk[e >> 1] = pack_bf16x2(p0, p1);
     }
-    tmem_st16(tS + c * 16, pk);  // over S values that have been read
+    tmem_st32(tS + h * 32, pk);  // over S values that have been read
   }
-  return make_float2(m_used, l + sum);
+  return make_float2(m_used, l + ((sum[0] + sum[1]) + (sum[2] + sum[3])));
+}
+
+// 8 consecutive 32-bit words of one row
+__device__ __forceinline__ void store8(void* p, const uint32_t* w, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    uint4* q = static_cast<uint4*>(p);
+    q[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    q[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
 }
 
 template <int D>
@@ -337,9 +328,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* pc_full = bars;                 // [NPC]
   uint64_t* pc_empty = pc_full + NPC;       // [NPC]
-  uint64_t* q_full = pc_empty + NPC;
-  uint64_t* q_empty = q_full + 1;
-  uint64_t* k_full = q_empty + 1;           // [SK]
+  uint64_t* q_full = pc_empty + NPC;        // [2] query tiles
+  uint64_t* q_empty = q_full + 2;           // [2]
+  uint64_t* k_full = q_empty + 2;           // [SK]
   uint64_t* k_empty = k_full + C::SK;       // [SK]
   uint64_t* v_full = k_empty + C::SK;       // [SV]
   uint64_t* v_empty = v_full + C::SV;       // [SV]
@@ -360,8 +351,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       mbar_init(&pc_full[i], 1);
       mbar_init(&pc_empty[i], 11);  // K, V, products, 8 softmax warps
     }
-    mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
     for (int i = 0; i < C::SK; ++i) {
       mbar_init(&k_full[i], 1);
       mbar_init(&k_empty[i], 1);
@@ -371,6 +360,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       mbar_init(&v_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);
       mbar_init(&o_full[i], 1);
@@ -383,28 +374,22 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   }
   if (warp == 3) tmem_alloc(tmem_slot, 512);
 
-  // ---- chunk size: the work in key tiles over the grid, the same in every CTA
-  int chunk;
-  {
-    long long* buf = reinterpret_cast<long long*>(xmax);
-    long long u = 0;
-    for (int s = threadIdx.x; s < a.pd.N; s += NTHREADS) {
-      const SeqLen q = seq_len_of(a.pd, a.q_start, a.kv_len, s, nullptr, false);
-      const Cut c = cut_of(a.pd, a.tpm, q, 0x7fffffff);
-      u += (long long)a.pd.Hkv * c.items * c.span;
-    }
-    u = block_sum(u, buf);
-    const long long want = (u + 2 * kGrid - 1) / (2 * kGrid);
-    chunk = (int)(want < 2 ? 2 : want > 0x3fffffff ? 0x3fffffff : want);
-    if (blockIdx.x == 0) {  // the merge reads how many items are split
-      long long ni = 0;
-      for (int s = threadIdx.x; s < a.pd.N; s += NTHREADS) {
-        const SeqLen q = seq_len_of(a.pd, a.q_start, a.kv_len, s, nullptr, false);
-        const Cut c = cut_of(a.pd, a.tpm, q, chunk);
-        ni += c.ns > 1 ? (long long)a.pd.Hkv * c.items : 0;
-      }
-      ni = block_sum(ni, buf);
-      if (threadIdx.x == 0) a.items[-4] = (int32_t)ni;
+  // ---- the line: its length, the part of it that waves would take, and the keys
+  // that several items share.  Exact integer sums, the same in every CTA.
+  unsigned long long* sums = reinterpret_cast<unsigned long long*>(xmax);
+  const unsigned grid = gridDim.x;
+  if (threadIdx.x < 3) sums[threadIdx.x] = 0;
+  Cut cut = cut_of(a, threadIdx.x, blockIdx.x == 0);  // (warp 0 keeps its 32)
+  __syncthreads();
+  for (int s = threadIdx.x; s < a.pd.N; s += NTHREADS) {
+    const Cut c = s < NTHREADS ? cut : cut_of(a, s, blockIdx.x == 0);
+    if (c.items == 0) continue;
+    atomicAdd(&sums[0], (unsigned long long)(c.head * a.pd.Hkv));
+    if (c.items > 1 && a.pd.window == 0) {
+      const unsigned all = (unsigned)c.items * (unsigned)a.pd.Hkv, in = all - all % grid;
+      const unsigned g = in / (unsigned)c.items;
+      atomicAdd(&sums[1], (unsigned long long)(c.head * g + item_at(c.A, c.B, (int)(in - g * c.items))));
+      atomicAdd(&sums[2], (unsigned long long)c.kv);
     }
   }
   tc_fence_before();
@@ -416,75 +401,196 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   if (warp == 0) {
     // ============================================================ pieces, Q
     if (lane == 0) tma_prefetch_desc(&mq);
-    Walk w;
-    w.p = blockIdx.x;
-    w.base = w.slots = w.items = 0;
-    w.s0 = 0;
-    walk_load(a, w, chunk);
-    int pub = 0, nq = 0, loads = 0;  // pieces published, their Q looked after, Q loads issued
-    bool done = false;
-    uint64_t t_prog = globaltimer();
+    const bool waves = (int64_t)sums[2] * a.pd.Hkv * (4 * D) > kWaveBytes;
+    const int64_t total = (int64_t)(sums[0] - (waves ? sums[1] : 0ull));
+    int64_t share = (total + grid - 1) / grid;
+    if (share < kLeastShare) share = kLeastShare;
+    int pub = 0, nq = 0;     // pieces published, their Q looked after
+    int qs = 0;              // query slot of the next single tile
+    uint32_t qph = 3u;       // phases of q_empty to wait for, bit = slot
+    uint32_t loaded = 0, lph = 0;  // slots with a load issued, its phase
+    // Q of the next piece, once its slots are free
+    auto pump = [&]() -> bool {
+      if (nq >= pub) return false;
+      const Piece& pc = piece_at(nq);
+      if (pc.n == 0) {
+        ++nq;
+        return true;
+      }
+      const uint32_t slots = pc.single ? 1u << qs : 3u;
+      for (int i = 0; i < 2; ++i)
+        if ((slots >> i & 1u) &&
+            !__shfl_sync(FULL, (int)mbar_test(&q_empty[i], (qph >> i) & 1u), 0))
+          return false;
+      if (lane == 0) {
+        int row = pc.row0;
+        for (int i = 0; i < 2; ++i) {
+          if (!(slots >> i & 1u)) continue;
+          mbar_expect_tx(&q_full[i], (uint32_t)(C::KC * 128 * a.pd.G * a.tpm));
+          for (int c = 0; c < C::KC; ++c)  // rows (token, head) of the box
+            tma_load_3d(smem + C::OFF_Q + i * C::TILE + c * (BM * 128), &mq, &q_full[i], c * 64,
+                        pc.g * a.pd.G, row);
+          row += a.tpm;
+        }
+      }
+      __syncwarp();
+      lph = (lph & ~slots) | (~qph & slots);  // a slot's n-th load completes phase n
+      qph ^= slots;
+      loaded |= slots;
+      if (pc.single) qs ^= 1;
+      ++nq;
+      return true;
+    };
+    // progress or, after a while without, the limit
+    uint64_t t_prog = 0;
     uint32_t idle = 0;
-    while (!done || nq < pub) {
-      bool progress = false;
-      if (!done && pub - nq < NPC &&
-          __shfl_sync(FULL, (int)mbar_test(&pc_empty[pub % NPC], (uint32_t)(((pub / NPC) & 1) ^ 1)),
-                      0)) {
-        Piece pc;
-        if (!walk_next(a, w, chunk, pc)) {
-          pc = Piece{};
-          pc.end = 1;
-          done = true;
-        }
-        if (lane == 0) {
-          piece_at(pub) = pc;
-          mbar_arrive(&pc_full[pub % NPC]);
-        }
-        __syncwarp();
-        ++pub;
-        progress = true;
-      }
-      if (nq < pub) {
-        const Piece& pc = piece_at(nq);
-        if (pc.n == 0) {
-          ++nq;
-          progress = true;
-        } else if (__shfl_sync(FULL, (int)mbar_test(q_empty, (uint32_t)((loads & 1) ^ 1)), 0)) {
-          if (lane == 0) {
-            const int tiles = pc.single ? 1 : 2;
-            mbar_expect_tx(q_full, (uint32_t)(tiles * C::KC * 128 * a.pd.G * a.tpm));
-            for (int i = 0; i < tiles; ++i)
-              for (int c = 0; c < C::KC; ++c)  // rows (token, head) of the box
-                tma_load_3d(smem + C::OFF_Q + i * C::TILE + c * (BM * 128), &mq, q_full, c * 64,
-                            pc.g * a.pd.G, pc.row0 + i * a.tpm);
-          }
-          __syncwarp();
-          ++loads;
-          ++nq;
-          progress = true;
-        }
-      }
+    auto waited = [&](bool progress) -> bool {
       if (progress) {
-        t_prog = globaltimer();
         idle = 0;
-      } else {
-        __nanosleep(64);
-        if ((++idle & 63) == 0) {
-          int stop = 0;
-          if (lane == 0) {
-            if (ab.set()) {
-              stop = 1;
-            } else if (globaltimer() - t_prog > kWaitLimitNs) {
-              ab.raise(a.status, 331);
-              stop = 1;
-            }
-          }
-          if (__shfl_sync(FULL, stop, 0)) break;
+        return true;
+      }
+      if (idle == 0) t_prog = globaltimer();
+      __nanosleep(64);
+      if ((++idle & 63) != 0) return true;
+      int stop = 0;
+      if (lane == 0) {
+        if (ab.set()) {
+          stop = 1;
+        } else if (globaltimer() - t_prog > kWaitLimitNs) {
+          ab.raise(a.status, 331);
+          stop = 1;
+        }
+      }
+      return !__shfl_sync(FULL, stop, 0);
+    };
+    auto publish = [&](const Piece& pc) -> bool {
+      for (;;) {
+        if (pub - nq < NPC &&
+            __shfl_sync(FULL, (int)mbar_test(&pc_empty[pub % NPC], (uint32_t)(((pub / NPC) & 1) ^ 1)),
+                        0))
+          break;
+        if (!waited(pump())) return false;
+      }
+      idle = 0;
+      if (lane == 0) {
+        piece_at(pub) = pc;
+        mbar_arrive(&pc_full[pub % NPC]);
+      }
+      __syncwarp();
+      ++pub;
+      pump();
+      return true;
+    };
+
+    bool ok = true;
+    int held = 0;  // the 32 requests this warp's lanes hold
+    auto hold = [&](int s0) {
+      if (held != s0) cut = cut_of(a, s0 + lane, false);
+      held = s0;
+    };
+    // items that go in waves, all KV groups of a request together
+    auto wave_items = [&](const Cut& c) -> unsigned {
+      if (!waves || c.items <= 1 || a.pd.window != 0) return 0u;
+      const unsigned all = (unsigned)c.items * (unsigned)a.pd.Hkv;
+      return all - all % grid;
+    };
+    if (waves) {
+      for (int s0 = 0; ok && s0 < a.pd.N; s0 += 32) {
+        hold(s0);
+        const unsigned in = wave_items(cut);
+        for (unsigned m = __ballot_sync(FULL, in > 0); ok && m; m &= m - 1) {
+          const int l = __ffs(m) - 1;
+          const int q0 = __shfl_sync(FULL, cut.q0, l), ql = __shfl_sync(FULL, cut.ql, l);
+          const int kv = __shfl_sync(FULL, cut.kv, l), ipt = __shfl_sync(FULL, cut.ipt, l);
+          const unsigned items = __shfl_sync(FULL, (unsigned)cut.items, l);
+          const unsigned lim = __shfl_sync(FULL, in, l);
+          for (unsigned f = blockIdx.x; ok && f < lim; f += grid)
+            ok = publish(item_piece(a, s0 + l, q0, ql, kv, ipt, (int)(f / items), (int)(f % items)));
         }
       }
     }
-    if (lane == 0 && ab.set() && loads > 0)
-      mbar_wait_drain(q_full, (uint32_t)((loads - 1) & 1), a.status, 391);
+    // this CTA's range of the line
+    const int64_t from = share * blockIdx.x;
+    const int64_t to = min(total, from + share);
+    int4 rec0 = make_int4(0, 0, 0, 0), rec1 = rec0;
+    int64_t base = 0;  // the place of the 32 requests
+    for (int s0 = 0; ok && s0 < a.pd.N && base < to; s0 += 32) {
+      hold(s0);
+      const unsigned in = wave_items(cut);
+      int64_t skip = 0;  // of the request's items, those in waves
+      if (in > 0) {
+        const unsigned g = in / (unsigned)cut.items;
+        skip = cut.head * g + item_at(cut.A, cut.B, (int)(in - g * cut.items));
+      }
+      const int64_t len = cut.head * a.pd.Hkv - skip;
+      const int64_t inc = lane_scan(len);
+      for (unsigned m = __ballot_sync(FULL, len > 0 && base + inc > from && base + inc - len < to);
+           ok && m; m &= m - 1) {
+        const int l = __ffs(m) - 1;
+        const int q0 = __shfl_sync(FULL, cut.q0, l), ql = __shfl_sync(FULL, cut.ql, l);
+        const int kv = __shfl_sync(FULL, cut.kv, l), ipt = __shfl_sync(FULL, cut.ipt, l);
+        const int items = __shfl_sync(FULL, cut.items, l);
+        const unsigned tw = __shfl_sync(FULL, (unsigned)cut.tw, l);
+        const int64_t A = __shfl_sync(FULL, cut.A, l), B = __shfl_sync(FULL, cut.B, l);
+        const int64_t head = __shfl_sync(FULL, cut.head, l);
+        // the request's own coordinate of the line's place 0
+        const int64_t zero = base + __shfl_sync(FULL, inc - len - skip, l);
+        const int64_t begin = max(from, base + __shfl_sync(FULL, inc - len, l)) - zero;
+        // the group and item that hold `begin`: an estimate, put right exactly
+        int g = (int)((float)begin / (float)head);
+        g = min(max(g, 0), a.pd.Hkv - 1);
+        while (g > 0 && head * g > begin) --g;
+        while (g < a.pd.Hkv - 1 && head * (g + 1) <= begin) ++g;
+        const float y = (float)(begin - head * g), fa = (float)A - 0.5f * (float)B, fb = (float)B;
+        int k = (int)(B == 0 ? y / fa : (sqrtf(fa * fa + 2.0f * fb * y) - fa) / fb);
+        k = min(max(k, 0), items - 1);
+        while (k > 0 && head * g + item_at(A, B, k) > begin) --k;
+        while (k < items - 1 && head * g + item_at(A, B, k + 1) <= begin) ++k;
+        int64_t at = zero + head * g + item_at(A, B, k);  // the item's place
+        while (ok && at < to) {
+          Piece pc = item_piece(a, s0 + l, q0, ql, kv, ipt, g, k);
+          const int64_t cost = A + B * k;
+          // tiles whose places lie in [from, to): places at, at + tw, ...
+          const int n = pc.n;
+          const int t0 = from > at ? (int)min((unsigned)n, ((unsigned)(from - at) + tw - 1) / tw) : 0;
+          const int t1 = to - at >= cost ? n : (int)min((unsigned)n, ((unsigned)(to - at) + tw - 1) / tw);
+          if (n == 0 ? at >= from : t1 > t0) {
+            pc.tb += t0;
+            pc.n = t1 - t0;
+            if (pc.n < n) {
+              pc.slot = 2 * blockIdx.x + (t0 > 0 ? 0 : 1);
+              if (t0 == 0) {  // begun here, continued by the CTAs up to the last tile's
+                int c = blockIdx.x;
+                const int64_t last = at + (int64_t)tw * (n - 1);
+                while (share * (c + 1) <= last) ++c;
+                rec0 = make_int4(pc.row0, pc.ntok, pc.g, 0);
+                rec1 = make_int4(c - (int)blockIdx.x + 1, 0, 0, 0);
+              }
+            }
+            ok = publish(pc);
+          }
+          at += cost;
+          if (++k == items) {
+            k = 0;
+            if (++g == a.pd.Hkv) break;
+          }
+        }
+      }
+      base += __shfl_sync(FULL, inc, 31);
+    }
+    if (lane == 0) {  // for the merge
+      a.rec[2 * blockIdx.x] = rec0;
+      a.rec[2 * blockIdx.x + 1] = rec1;
+    }
+    if (ok) {
+      Piece pc{};
+      pc.end = 1;
+      ok = publish(pc);
+    }
+    while (ok && nq < pub) ok = waited(pump());
+    if (lane == 0 && ab.set())
+      for (int i = 0; i < 2; ++i)
+        if (loaded >> i & 1u) mbar_wait_drain(&q_full[i], (lph >> i) & 1u, a.status, 391);
   } else if (warp <= 2) {
     // ========================================================== K or V loads
     const bool isK = warp == 1;
@@ -557,7 +663,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     int ks = 0, vs = 0;             // slots of the next key tile
     uint32_t kph = 0, vph = 0;      // and their phases
     uint32_t pph = 0;               // phases of p_full, bit = group
-    uint32_t qph = 0;               // phase of q_full
+    int qs = 0;                     // query slot of the next single tile
+    uint32_t qph = 0;               // phases of q_full, bit = slot
     bool first = true, ok = true;
     for (int i = 0; ok; ++i) {
       ok = warp_poll(&pc_full[i % NPC], (uint32_t)((i / NPC) & 1), ab, a.status, 335);
@@ -567,26 +674,28 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       const int n = __reduce_max_sync(FULL, pc.n), single = __reduce_max_sync(FULL, pc.single);
       const int end = __reduce_max_sync(FULL, pc.end);
       if (n > 0) {
-        ok = warp_poll(q_full, qph, ab, a.status, 336);
+        ok = warp_poll(&q_full[single ? qs : 0], (qph >> (single ? qs : 0)) & 1u, ab, a.status, 336) &&
+             (single || warp_poll(&q_full[1], qph >> 1, ab, a.status, 336));
         // Debug request (host-set status[3]): the first piece waits on a barrier
         // nothing arrives on, so the pipeline gives up (detail 220) while its K
         // and V copies are in flight.
         if (ok && first && blockIdx.x == 0 && debug_request(a.status) == SGQA_DEBUG_STALL)
           ok = __all_sync(FULL, mbar_wait(stall_bar, 0, ab, a.status, 220, kDebugStallNs));
         if (!ok) break;
-        qph ^= 1;
+        qph ^= single ? 1u << qs : 3u;
         first = false;
       }
       if (leader) mbar_arrive(&pc_empty[i % NPC]);
       if (end) break;
       const int sh = single ? 0 : 1;  // a key tile serves 1 << sh products of each kind
       const int J = n << sh;
+      const int slot = single ? qs : 0;  // of the first query tile
       // S of step j: group j & 1, query tile j & sh, the next key tile when j & sh is 0
       auto do_qk = [&](int j) -> bool {
         if ((j & sh) == 0 && !warp_poll(&k_full[ks], kph, ab, a.status, 337)) return false;
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)(j & 1) * 128;
-        const uint32_t la = lq + (uint32_t)(j & sh) * (C::TILE / 16), lb = lk + (uint32_t)ks * (C::TILE / 16);
+        const uint32_t la = lq + (uint32_t)(slot + (j & sh)) * (C::TILE / 16), lb = lk + (uint32_t)ks * (C::TILE / 16);
         if (leader) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
@@ -595,7 +704,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           }
           umma_commit(&s_full[j & 1]);
           if ((j & sh) == sh) umma_commit(&k_empty[ks]);
-          if (j == J - 1) umma_commit(q_empty);
+          if (j >= J - 1 - sh) umma_commit(&q_empty[slot + (j & sh)]);  // its last product
         }
         __syncwarp();
         if ((j & sh) == sh && ++ks == C::SK) {
@@ -631,6 +740,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         // only after the product above has read it
         if (j + 2 < J) ok = do_qk(j + 2);
       }
+      if (single && n > 0) qs ^= 1;
     }
     if (leader) {
       umma_commit(mma_done);
@@ -789,17 +899,16 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             ov[e] = (use0 && g0 > 0.0f ? __uint_as_float(o0[e]) * g0 : 0.0f) +
                     (use1 && g1 > 0.0f ? __uint_as_float(o1[e]) * g1 : 0.0f);
           if (row_ok && pc.slot >= 0) {
-            float* dst = a.opart + prow * D + c * 32;
+            uint32_t* dst = reinterpret_cast<uint32_t*>(a.opart + prow * D + c * 32);
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<float4*>(dst + e) = make_float4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
+            for (int e = 0; e < 32; e += 8) store8(dst + e, reinterpret_cast<uint32_t*>(ov) + e, true);
           } else if (row_ok) {
-            __nv_bfloat16* dst = a.O + orow * D + c * 32;
+            uint32_t* dst = reinterpret_cast<uint32_t*>(a.O + orow * D + c * 32);
+            uint32_t w[16];
 #pragma unroll
-            for (int e = 0; e < 32; e += 8)
-              *reinterpret_cast<uint4*>(dst + e) =
-                  make_uint4(pack_bf16x2(ov[e], ov[e + 1]), pack_bf16x2(ov[e + 2], ov[e + 3]),
-                             pack_bf16x2(ov[e + 4], ov[e + 5]), pack_bf16x2(ov[e + 6], ov[e + 7]));
+            for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(ov[2 * e], ov[2 * e + 1]);
+            store8(dst, w, a.wide);
+            store8(dst + 8, w + 8, a.wide);
           }
           __syncwarp();  // the loads from tensor memory are warp-wide
         }
@@ -827,54 +936,66 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   }
 }
 
-// Merge of the split items' partial outputs in chunk order: lse = ln sum e^(lse_j),
-// O = sum e^(lse_j - lse) O_j.  A warp per row; a CTA takes 8 rows of an item.
+// Merge of the cut items' partial outputs in order: lse = ln sum e^(lse_j), O =
+// sum e^(lse_j - lse) O_j.  The item that CTA c begins has its parts in slots 2 c +
+// 1, 2 c + 2, 2 c + 4, ...  A warp per row, all rows of all cut items dealt out
+// evenly.
 template <int D>
 __global__ void __launch_bounds__(256) k_paged_merge(const __grid_constant__ TcArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int n_items = a.items[-4];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int blocks = (a.slot_rows + 7) / 8;
+  const int lane = threadIdx.x & 31;
+  const int warps = gridDim.x * 8;
+  int row = blockIdx.x * 8 + (threadIdx.x >> 5);  // among the rows still to come
   const float ninf = -__int_as_float(0x7f800000);
-  for (int64_t u = blockIdx.x; u < (int64_t)n_items * blocks; u += gridDim.x) {
-    const int4* rec = reinterpret_cast<const int4*>(a.items) + 2 * (u / blocks);
-    const int4 r0 = rec[0], r1 = rec[1];
-    const int row = (int)(u % blocks) * 8 + warp;
-    if (row >= r0.y * a.pd.G) continue;
-    const int tok = row / a.pd.G, h = row - tok * a.pd.G;
-    const int tile = tok / a.tpm;  // rows of the second query tile start at BM
-    const int64_t at = (int64_t)r1.x * a.slot_rows + tile * BM + (tok - tile * a.tpm) * a.pd.G + h;
-    const int64_t stride = (int64_t)r1.y * a.slot_rows;
-    float mx = ninf;
-    for (int j = lane; j < r1.z; j += 32) mx = fmaxf(mx, a.lpart[at + j * stride]);
+  constexpr int W = D / 32;
+  for (int c0 = 0; c0 < kGrid; c0 += 32) {
+    int mine = 0;
+    if (c0 + lane < kGrid && a.rec[2 * (c0 + lane) + 1].x > 1) mine = a.rec[2 * (c0 + lane)].y * a.pd.G;
+    for (unsigned m = __ballot_sync(FULL, mine > 0); m; m &= m - 1) {
+      const int l = __ffs(m) - 1, rows = __shfl_sync(FULL, mine, l);
+      for (; row < rows; row += warps) {
+        const int4 r0 = a.rec[2 * (c0 + l)];
+        const int parts = a.rec[2 * (c0 + l) + 1].x;
+        const int tok = row / a.pd.G, h = row - tok * a.pd.G;
+        const int tile = tok / a.tpm;  // rows of the second query tile start at BM
+        const int at = tile * BM + (tok - tile * a.tpm) * a.pd.G + h;
+        const int64_t first = 2 * (int64_t)(c0 + l);
+        auto place = [&](int j) { return (first + (j == 0 ? 1 : 2 * j)) * a.slot_rows + at; };
+        float mx = ninf;
+        for (int j = lane; j < parts; j += 32) mx = fmaxf(mx, a.lpart[place(j)]);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, o));
-    float acc[D / 32], sw = 0.0f;
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, o));
+        float acc[W], sw = 0.0f;
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) acc[e] = 0.0f;
-    for (int j = 0; j < r1.z; ++j) {
-      const float lj = a.lpart[at + j * stride];
-      if (lj == ninf) continue;  // nothing seen in this chunk
-      const float w = expf(lj - mx);
-      sw += w;
+        for (int e = 0; e < W; ++e) acc[e] = 0.0f;
+#pragma unroll 4
+        for (int j = 0; j < parts; ++j) {
+          const float lj = a.lpart[place(j)];
+          const float w = lj == ninf ? 0.0f : __expf(lj - mx);
+          const float* src = a.opart + place(j) * D + lane * W;
+          float v[W];
+          if constexpr (W == 4)
+            *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(src);
+          else
+            *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(src);
+          sw += w;
 #pragma unroll
-      for (int e = 0; e < D / 32; ++e)
-        acc[e] = fmaf(w, a.opart[(at + j * stride) * D + lane * (D / 32) + e], acc[e]);
+          for (int e = 0; e < W; ++e) acc[e] = fmaf(w, v[e], acc[e]);  // (parts that saw nothing hold 0)
+        }
+        const float inv = sw > 0.0f ? 1.0f / sw : 0.0f;
+        const int64_t t = r0.x + tok;
+        const int64_t hq = (int64_t)r0.z * a.pd.G + h;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(a.O + (t * a.pd.H + hq) * D + lane * W);
+#pragma unroll
+        for (int e = 0; e < W / 2; ++e) dst[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+        if (lane == 0) a.lse[hq * a.pd.T + t] = sw > 0.0f ? mx + logf(sw) : ninf;
+      }
+      row -= rows;
     }
-    const float inv = sw > 0.0f ? 1.0f / sw : 0.0f;
-    const int64_t t = r0.x + tok;
-    const int64_t hq = (int64_t)r0.z * a.pd.G + h;
-    __nv_bfloat16* dst = a.O + (t * a.pd.H + hq) * D + lane * (D / 32);
-#pragma unroll
-    for (int e = 0; e < D / 32; e += 2)
-      *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-    if (lane == 0) a.lse[hq * a.pd.T + t] = sw > 0.0f ? mx + logf(sw) : ninf;
   }
 }
 
-// Most partial outputs of a call: a split item of n key tiles has fewer than 2 n /
-// chunk chunks, and chunk is at least 1 / (2 kGrid) of all tiles.
-constexpr int kSlots = 2 * 2 * kGrid;
+constexpr int kSlots = 2 * kGrid;  // the first and the last piece of a CTA
 
 int slot_rows(const PagedDims& pd) {
   const int64_t rows = (int64_t)pd.T * pd.G;
@@ -882,13 +1003,12 @@ int slot_rows(const PagedDims& pd) {
 }
 
 struct Ws {
-  size_t items, lpart, opart, bytes;
+  size_t lpart, opart, bytes;
 };
 Ws carve(const PagedDims& pd) {
   Ws w;
   const size_t rows = (size_t)kSlots * slot_rows(pd);
-  w.items = 256;  // the number of items stands before them
-  w.lpart = w.items + (((size_t)kSlots * 32 + 255) & ~size_t(255));
+  w.lpart = ((size_t)kGrid * 32 + 255) & ~size_t(255);
   w.opart = w.lpart + ((rows * 4 + 255) & ~size_t(255));
   w.bytes = w.opart + rows * pd.d * 4;
   return w;
@@ -955,7 +1075,7 @@ int launch_paged_tc(const PagedDims& pd, const PagedAttnArgs& pa, void* ws, cuda
   a.kv_len = pa.kv_len;
   a.O = static_cast<__nv_bfloat16*>(pa.O);
   a.lse = pa.lse;
-  a.items = reinterpret_cast<int32_t*>(base + w.items);
+  a.rec = reinterpret_cast<int4*>(base);
   a.lpart = reinterpret_cast<float*>(base + w.lpart);
   a.opart = reinterpret_cast<float*>(base + w.opart);
   a.status = pa.status;
@@ -968,7 +1088,12 @@ int launch_paged_tc(const PagedDims& pd, const PagedAttnArgs& pa, void* ws, cuda
   }
   a.box = x;
   a.tpm = BM / pd.G;
+  a.wide = (reinterpret_cast<uintptr_t>(pa.O) & 31u) == 0;
   a.sl2 = pd.scale * 1.4426950408889634f;
+  // windows and lengths end at cap: the sums of both stay in 32 bits
+  if (a.pd.window > pd.cap) a.pd.window = pd.cap;
+  // whole items of a request, over its KV groups, are counted in 32 bits
+  if ((int64_t)pd.Hkv * ((int64_t)pd.T / a.tpm + 1) > 0x7fffffffll) return SGQA_ERR_UNSUPPORTED;
   return pd.d == 128 ? launch<128>(a, pa, st) : launch<64>(a, pa, st);
 }
 
