@@ -55,8 +55,14 @@ struct Cfg {
   static constexpr int OFF_X = OFF_V + SV * TILE;      // maxima and sums [2][2][BM] floats
   static constexpr int OFF_PC = OFF_X + 4 * BM * 4;    // piece ring
   static constexpr int OFF_BAR = OFF_PC + NPC * 64;
-  static constexpr int NBAR = 2 * NPC + 4 + 2 * SK + 2 * SV + 6 + 4;
+  static constexpr int NBAR = 2 * NPC + 4 + 2 * SK + 2 * SV + 10 + 4;
   static constexpr int SMEM = OFF_BAR + NBAR * 8 + 64;
+  // Tensor memory columns: S of the groups at 0 and 128; with d = 64 there is room
+  // for P beside S, so the next S can be computed as soon as the last one has been
+  // read; with d = 128 P lies over S.
+  static constexpr bool OWN_P = D == 64;
+  static constexpr int TP = OWN_P ? 256 : 0, TP_STEP = OWN_P ? 64 : 128;
+  static constexpr int TO = OWN_P ? 384 : 256, TO_STEP = D;
   static_assert(SMEM <= 232448, "shared memory of one CTA");
 };
 
@@ -66,7 +72,8 @@ struct TcArgs {
   __nv_bfloat16* O;
   float* lse;
   float *opart, *lpart;  // partial outputs [slot][slot_rows][D], their lse [slot][slot_rows]
-  int4* rec;             // [kGrid][2]: the item that CTA c begins and another ends
+  int4* rec;             // [kGrid]: row0, tokens, group and parts of the item that CTA c
+                         // begins and another ends
   int32_t* status;
   int slot_rows;
   int box;               // rows of a K/V box: gcd(page size, 128)
@@ -94,6 +101,10 @@ constexpr int kWtSingle = 2, kWtDouble = 3;
 constexpr int kOver = 3;
 // Shortest range of a CTA, in line units: two key tiles of a single query tile.
 constexpr int64_t kLeastShare = 2 * KB * kWtSingle;
+// A range that ends within kSnap tiles of an item's beginning or end leaves the
+// item whole, when ranges are long enough for that to leave no part empty.
+constexpr int kSnap = 2;
+constexpr int64_t kSnapShare = (int64_t)8 * KB * kWtDouble;
 // K and V bytes of the requests with several items above which waves are used:
 // about half of L2.
 constexpr int64_t kWaveBytes = int64_t(64) << 20;
@@ -170,25 +181,9 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Bounded wait that polls: for the hand-offs of the product pipeline, where a
-// suspended wait's wake-up costs more than the polling.
-__device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, const Abort& ab,
-                                          int32_t* status, int where) {
-  if (mbar_test(bar, parity)) return true;
-  const uint64_t t0 = globaltimer();
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_test(bar, parity)) return true;
-    if ((i & 255) == 0) {
-      if (ab.set()) return false;
-      if (globaltimer() - t0 > kWaitLimitNs) {
-        ab.raise(status, where);
-        return false;
-      }
-    }
-  }
-}
-
-// The same for a whole warp, with a warp-uniform outcome.
+// Bounded wait of a whole warp that polls, with a warp-uniform outcome: for the
+// hand-offs of the product pipeline, where a suspended wait's wake-up costs more
+// than the polling.
 __device__ __forceinline__ bool warp_poll(uint64_t* bar, uint32_t parity, const Abort& ab,
                                           int32_t* status, int where) {
   if (__all_sync(FULL, mbar_test(bar, parity))) return true;
@@ -237,9 +232,10 @@ __device__ __forceinline__ uint32_t seen_bits(int k, int lo, int hi) {
 
 // A tile in two passes: its masked maximum, then the weights; raises the
 // reference maximum and rescales what was accumulated under the old one.
-// S (128 columns at tS) is overwritten by P.  Returns the maximum and the sum.
+// S is 128 columns at tS, P 64 at tP (which may be the first of S's).  Returns the
+// maximum and the sum.
 template <int D>
-__device__ __noinline__ float2 tile_two_pass(uint32_t tS, uint32_t tO, float sl2, uint32_t a0,
+__device__ __noinline__ float2 tile_two_pass(uint32_t tS, uint32_t tP, uint32_t tO, float sl2, uint32_t a0,
                                              uint32_t a1, uint32_t a2, uint32_t a3, bool have_o,
                                              float m_used, float l) {
   const float ninf = -__int_as_float(0x7f800000);
@@ -293,9 +289,45 @@ __device__ __noinline__ float2 tile_two_pass(uint32_t tS, uint32_t tO, float sl2
       sum[(e & 2) + 1] += p1;
       pk[e >> 1] = pack_bf16x2(p0, p1);
     }
-    tmem_st32(tS + h * 32, pk);  // over S values that have been read
+    tmem_st32(tP + h * 32, pk);  // (over S values that have been read)
   }
   return make_float2(m_used, l + ((sum[0] + sum[1]) + (sum[2] + sum[3])));
+}
+
+// The weights of a tile under the reference maximum -nm, packed, and their sum
+// (two packed sums of two).  MASK: am holds a bit for each key the row sees.
+// after_read: called once S is in registers.
+template <bool MASK, typename F>
+__device__ __forceinline__ float tile_weights(uint32_t tS, uint64_t sl2x2, float nm,
+                                              const uint32_t (&am)[4], uint32_t (&pk)[64],
+                                              F after_read) {
+  const float ninf = -__int_as_float(0x7f800000);
+  const uint64_t nm2 = f2_pack(nm, nm);
+  uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t v[64];
+    tmem_ld32(tS + h * 64, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
+    tmem_ld32(tS + h * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
+    tmem_wait_ld();
+    if (h == 1) after_read();
+#pragma unroll
+    for (int e = 0; e < 64; e += 2) {
+      float x0, x1;
+      f2_unpack(f2_fma(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sl2x2, nm2), x0, x1);
+      if constexpr (MASK) {  // by selection: S of keys outside the cache may be NaN
+        const uint32_t m = am[2 * h + (e >> 5)];
+        x0 = ((m >> (e & 31)) & 1u) ? x0 : ninf;
+        x1 = ((m >> ((e & 31) + 1)) & 1u) ? x1 : ninf;
+      }
+      const float p0 = ex2(x0), p1 = ex2(x1);
+      acc[(e >> 1) & 3] = f2_add(acc[(e >> 1) & 3], f2_pack(p0, p1));
+      pk[h * 32 + (e >> 1)] = pack_bf16x2(p0, p1);
+    }
+  }
+  float s0, s1;
+  f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), s0, s1);
+  return s0 + s1;
 }
 
 // 8 consecutive 32-bit words of one row
@@ -336,7 +368,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   uint64_t* v_empty = v_full + C::SV;       // [SV]
   uint64_t* s_full = v_empty + C::SV;       // [2] S of a group's key tile
   uint64_t* p_full = s_full + 2;            // [2] its P
-  uint64_t* o_full = p_full + 2;            // [2] a group's last product of a piece done
+  uint64_t* s_empty = p_full + 2;           // [2] S has been read (OWN_P)
+  uint64_t* p_empty = s_empty + 2;          // [2] the product with P is done (OWN_P)
+  uint64_t* o_full = p_empty + 2;           // [2] a group's last product of a piece done
   uint64_t* x_bar = o_full + 2;             // [2] groups joined: statistics, outputs read
   uint64_t* mma_done = x_bar + 2;
   uint64_t* stall_bar = mma_done + 1;       // nothing arrives on it
@@ -364,6 +398,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       mbar_init(&q_empty[i], 1);
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);
+      mbar_init(&s_empty[i], 4);
+      mbar_init(&p_empty[i], 1);
       mbar_init(&o_full[i], 1);
       mbar_init(&x_bar[i], 8);
     }
@@ -376,20 +412,33 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 
   // ---- the line: its length, the part of it that waves would take, and the keys
   // that several items share.  Exact integer sums, the same in every CTA.
-  unsigned long long* sums = reinterpret_cast<unsigned long long*>(xmax);
+  int64_t* sums = reinterpret_cast<int64_t*>(xmax);  // [warp][3]
   const unsigned grid = gridDim.x;
-  if (threadIdx.x < 3) sums[threadIdx.x] = 0;
   Cut cut = cut_of(a, threadIdx.x, blockIdx.x == 0);  // (warp 0 keeps its 32)
-  __syncthreads();
-  for (int s = threadIdx.x; s < a.pd.N; s += NTHREADS) {
-    const Cut c = s < NTHREADS ? cut : cut_of(a, s, blockIdx.x == 0);
-    if (c.items == 0) continue;
-    atomicAdd(&sums[0], (unsigned long long)(c.head * a.pd.Hkv));
-    if (c.items > 1 && a.pd.window == 0) {
-      const unsigned all = (unsigned)c.items * (unsigned)a.pd.Hkv, in = all - all % grid;
-      const unsigned g = in / (unsigned)c.items;
-      atomicAdd(&sums[1], (unsigned long long)(c.head * g + item_at(c.A, c.B, (int)(in - g * c.items))));
-      atomicAdd(&sums[2], (unsigned long long)c.kv);
+  {
+    int64_t line = 0, wave = 0, keys = 0;
+    for (int s = threadIdx.x; s < a.pd.N; s += NTHREADS) {
+      const Cut c = s < NTHREADS ? cut : cut_of(a, s, blockIdx.x == 0);
+      line += c.head * a.pd.Hkv;
+      if (c.items > 1 && a.pd.window == 0) {
+        const unsigned all = (unsigned)c.items * (unsigned)a.pd.Hkv, in = all - all % grid;
+        const unsigned g = in / (unsigned)c.items;
+        wave += c.head * g + item_at(c.A, c.B, (int)(in - g * c.items));
+        keys += c.kv;
+      }
+    }
+    if (warp * 32 < a.pd.N) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        line += __shfl_xor_sync(FULL, line, o);
+        wave += __shfl_xor_sync(FULL, wave, o);
+        keys += __shfl_xor_sync(FULL, keys, o);
+      }
+    }
+    if (lane == 0) {
+      sums[warp * 3] = line;
+      sums[warp * 3 + 1] = wave;
+      sums[warp * 3 + 2] = keys;
     }
   }
   tc_fence_before();
@@ -397,12 +446,21 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const Abort ab{abort_flag};
+  // The others sleep until the first piece is there: waiting on its barrier they
+  // slowed the walk of warp 0 from 2 to 12 thousand cycles.
+  if (warp != 0) asm volatile("bar.sync 1, 384;" ::: "memory");
 
   if (warp == 0) {
     // ============================================================ pieces, Q
     if (lane == 0) tma_prefetch_desc(&mq);
-    const bool waves = (int64_t)sums[2] * a.pd.Hkv * (4 * D) > kWaveBytes;
-    const int64_t total = (int64_t)(sums[0] - (waves ? sums[1] : 0ull));
+    int64_t line = 0, in_waves = 0, keys = 0;
+    for (int i = 0; i < NTHREADS / 32 && i * 32 < a.pd.N; ++i) {
+      line += sums[i * 3];
+      in_waves += sums[i * 3 + 1];
+      keys += sums[i * 3 + 2];
+    }
+    const bool waves = keys * a.pd.Hkv * (4 * D) > kWaveBytes;
+    const int64_t total = line - (waves ? in_waves : 0);
     int64_t share = (total + grid - 1) / grid;
     if (share < kLeastShare) share = kLeastShare;
     int pub = 0, nq = 0;     // pieces published, their Q looked after
@@ -477,6 +535,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         mbar_arrive(&pc_full[pub % NPC]);
       }
       __syncwarp();
+      if (pub == 0) asm volatile("bar.arrive 1, 384;" ::: "memory");
       ++pub;
       pump();
       return true;
@@ -512,7 +571,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     // this CTA's range of the line
     const int64_t from = share * blockIdx.x;
     const int64_t to = min(total, from + share);
-    int4 rec0 = make_int4(0, 0, 0, 0), rec1 = rec0;
+    int4 rec = make_int4(0, 0, 0, 0);
     int64_t base = 0;  // the place of the 32 requests
     for (int s0 = 0; ok && s0 < a.pd.N && base < to; s0 += 32) {
       hold(s0);
@@ -552,8 +611,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           const int64_t cost = A + B * k;
           // tiles whose places lie in [from, to): places at, at + tw, ...
           const int n = pc.n;
-          const int t0 = from > at ? (int)min((unsigned)n, ((unsigned)(from - at) + tw - 1) / tw) : 0;
-          const int t1 = to - at >= cost ? n : (int)min((unsigned)n, ((unsigned)(to - at) + tw - 1) / tw);
+          auto tiles_before = [&](int64_t x) -> int {  // places before x, ends snapped
+            if (x <= at) return 0;
+            if (x - at >= cost) return n;
+            const int t = (int)min((unsigned)n, ((unsigned)(x - at) + tw - 1) / tw);
+            return share < kSnapShare ? t : t <= kSnap ? 0 : t >= n - kSnap ? n : t;
+          };
+          const int t0 = tiles_before(from), t1 = tiles_before(to);
           if (n == 0 ? at >= from : t1 > t0) {
             pc.tb += t0;
             pc.n = t1 - t0;
@@ -561,10 +625,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
               pc.slot = 2 * blockIdx.x + (t0 > 0 ? 0 : 1);
               if (t0 == 0) {  // begun here, continued by the CTAs up to the last tile's
                 int c = blockIdx.x;
-                const int64_t last = at + (int64_t)tw * (n - 1);
-                while (share * (c + 1) <= last) ++c;
-                rec0 = make_int4(pc.row0, pc.ntok, pc.g, 0);
-                rec1 = make_int4(c - (int)blockIdx.x + 1, 0, 0, 0);
+                while (tiles_before(min(total, share * (c + 1))) < n) ++c;
+                rec = make_int4(pc.row0, pc.ntok, pc.g, c - (int)blockIdx.x + 1);
               }
             }
             ok = publish(pc);
@@ -578,10 +640,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
       base += __shfl_sync(FULL, inc, 31);
     }
-    if (lane == 0) {  // for the merge
-      a.rec[2 * blockIdx.x] = rec0;
-      a.rec[2 * blockIdx.x + 1] = rec1;
-    }
+    if (lane == 0) a.rec[blockIdx.x] = rec;  // for the merge
     if (ok) {
       Piece pc{};
       pc.end = 1;
@@ -662,7 +721,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const uint32_t lv = (smem_u32(smem + C::OFF_V) >> 4) | ((uint32_t)(KB * 128 / 16) << 16);
     int ks = 0, vs = 0;             // slots of the next key tile
     uint32_t kph = 0, vph = 0;      // and their phases
-    uint32_t pph = 0;               // phases of p_full, bit = group
+    uint32_t pph = 0, sph = 0;      // phases of p_full and s_empty, bit = group
     int qs = 0;                     // query slot of the next single tile
     uint32_t qph = 0;               // phases of q_full, bit = slot
     bool first = true, ok = true;
@@ -716,18 +775,26 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       ok = J == 0 || (do_qk(0) && (J < 2 || do_qk(1)));
       for (int j = 0; ok && j < J; ++j) {
         const int grp = j & 1;
+        if constexpr (C::OWN_P) {  // the next S as soon as this one has been read
+          ok = warp_poll(&s_empty[grp], (sph >> grp) & 1u, ab, a.status, 347);
+          sph ^= 1u << grp;
+          if (ok && j + 2 < J) ok = do_qk(j + 2);
+          if (!ok) break;
+        }
         ok = ((j & sh) != 0 || warp_poll(&v_full[vs], vph, ab, a.status, 338)) &&
              warp_poll(&p_full[grp], (pph >> grp) & 1u, ab, a.status, 339);
         if (!ok) break;
         pph ^= 1u << grp;
         tc_fence_after();
-        const uint32_t d = tmem + 256 + (uint32_t)grp * 128, pa = tmem + (uint32_t)grp * 128;
+        const uint32_t d = tmem + C::TO + (uint32_t)grp * C::TO_STEP;
+        const uint32_t pa = tmem + C::TP + (uint32_t)grp * C::TP_STEP;
         const uint32_t lb = lv + (uint32_t)vs * (C::TILE / 16);
         const uint32_t more = j > 1;
         if (leader) {
 #pragma unroll
           for (int kk = 0; kk < KB / 16; ++kk)
             umma_ts(d, pa + kk * 8, lb + kk * 128, idesc_pv, kk > 0 ? 1u : more);
+          if constexpr (C::OWN_P) umma_commit(&p_empty[grp]);
           if ((j & sh) == sh) umma_commit(&v_empty[vs]);
           if (j + 2 >= J) umma_commit(&o_full[grp]);  // the group's last product
         }
@@ -738,7 +805,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
         // products of one thread run in issue order, so this S overwrites P
         // only after the product above has read it
-        if (j + 2 < J) ok = do_qk(j + 2);
+        if constexpr (!C::OWN_P) {
+          if (j + 2 < J) ok = do_qk(j + 2);
+        }
       }
       if (single && n > 0) qs ^= 1;
     }
@@ -752,7 +821,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const int grp = (warp - 4) >> 2, quad = warp & 3;
     const int r = quad * 32 + lane;
     const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    const uint32_t tS = tl + grp * 128, tO = tl + 256 + grp * 128;
+    const uint32_t tS = tl + grp * 128, tP = tl + C::TP + grp * C::TP_STEP;
+    const uint32_t tO = tl + C::TO + grp * C::TO_STEP;
     const float ninf = -__int_as_float(0x7f800000);
     const float sl2 = a.sl2;
     const uint64_t sl2x2 = f2_pack(sl2, sl2);
@@ -776,54 +846,86 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       const int step = pc.single ? 2 : 1;
       const int t0 = pc.single ? grp : 0;
       for (int t = t0; t < pc.n; t += step) {
-        ok = __all_sync(FULL, mbar_poll(&s_full[grp], (uint32_t)(sc & 1), ab, a.status, 341));
+        ok = __all_sync(FULL, mbar_wait(&s_full[grp], (uint32_t)(sc & 1), ab, a.status, 341));
         if (!ok) break;
         ++sc;
         tc_fence_after();
         const int k0 = (pc.tb + t) * KB;
+        // S has been read: with its own P, the next one may be computed
+        auto s_read = [&]() {
+          if constexpr (C::OWN_P) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_empty[grp]);
+          }
+        };
+        // ... and P may be written once the last product with it is done
+        auto p_free = [&]() -> bool {
+          if constexpr (C::OWN_P) {
+            if (sc == 1) return true;
+            return __all_sync(FULL, mbar_wait(&p_empty[grp], (uint32_t)(sc & 1), ab, a.status, 348));
+          }
+          return true;
+        };
         if (active) {
           const bool whole = __all_sync(FULL, lo <= k0 && k0 + KB <= hi);
-          bool fast = whole && __all_sync(FULL, m_used != ninf || !row_ok);
+          uint32_t am[4] = {FULL, FULL, FULL, FULL};
+          if (!whole) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) am[w] = seen_bits(k0 + 32 * w, lo, hi);
+          }
+          const bool none = !row_ok || (am[0] | am[1] | am[2] | am[3]) == 0u;
+          // A row's first keys: the reference is the maximum of 32 of them (of the
+          // tile's end where a window begins in it); the sum below shows whether
+          // the others exceed it by much.
+          if (__any_sync(FULL, m_used == ninf && !none)) {
+            const int c = pc.lo > k0 ? 3 : 0;
+            uint32_t v[32];
+            tmem_ld32(tS + c * 32, v);
+            tmem_wait_ld();
+            float mx[4] = {ninf, ninf, ninf, ninf};
+            const uint32_t m = c == 0 ? am[0] : am[3];
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              mx[e & 3] = fmaxf(mx[e & 3], ((m >> e) & 1u) ? __uint_as_float(v[e]) : ninf);
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+            if (m_used == ninf) m_used = top;
+          }
+          bool fast = __all_sync(FULL, m_used != ninf || none);
+          const float nm = m_used == ninf ? 0.0f : -m_used;
+          bool read = false;
           if (fast) {
             // One pass under the reference maximum; P is written only if the
             // tile's weights sum to at most kLazySum in every row.
-            const float nm = row_ok ? -m_used : ninf;
-            const uint64_t nm2 = f2_pack(nm, nm);
-            uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
             uint32_t pk[64];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t v[64];
-              tmem_ld32(tS + h * 64, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
-              tmem_ld32(tS + h * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
-              tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 64; e += 2) {
-                float x0, x1;
-                f2_unpack(f2_fma(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sl2x2,
-                                 nm2), x0, x1);
-                const float p0 = ex2(x0), p1 = ex2(x1);
-                acc[(e >> 1) & 3] = f2_add(acc[(e >> 1) & 3], f2_pack(p0, p1));
-                pk[h * 32 + (e >> 1)] = pack_bf16x2(p0, p1);
-              }
-            }
-            float s0, s1;
-            f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), s0, s1);
-            const float sum = s0 + s1;
+            float sum;
+            auto keep = [&]() {};
+            if (whole)
+              sum = tile_weights<false>(tS, sl2x2, nm, am, pk, keep);
+            else
+              sum = tile_weights<true>(tS, sl2x2, nm, am, pk, keep);
             fast = __all_sync(FULL, sum <= kLazySum || !row_ok);
             if (fast) {
-              tmem_st32(tS, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
-              tmem_st32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
+              s_read();
+              read = true;
+              ok = p_free();
+              if (!ok) break;
+              tmem_st32(tP, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
+              tmem_st32(tP + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
               l += sum;
             }
           }
           if (!fast) {
-            const float2 ml = tile_two_pass<D>(
-                tS, tO, sl2, seen_bits(k0, lo, hi), seen_bits(k0 + 32, lo, hi),
-                seen_bits(k0 + 64, lo, hi), seen_bits(k0 + 96, lo, hi), t > t0, m_used, l);
+            ok = p_free();
+            if (!ok) break;
+            const float2 ml =
+                tile_two_pass<D>(tS, tP, tO, sl2, am[0], am[1], am[2], am[3], t > t0, m_used, l);
             m_used = ml.x;
             l = ml.y;
           }
+          if (!read) s_read();
+        } else {
+          s_read();
         }
         // Rows of V that no row of the item sees are zeroed before the product:
         // they may hold anything, and 0 times an infinity or NaN would count.
@@ -834,8 +936,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           if (k0 + r < pc.lo || k0 + r >= pc.hi) {
             uint8_t* vr = smem + C::OFF_V + vs * C::TILE + r * 128;
             for (int c = 0; c < C::KC; ++c)
-              for (int b = 0; b < 128; b += 16)
-                *reinterpret_cast<uint4*>(vr + c * (KB * 128) + b) = make_uint4(0, 0, 0, 0);
+#pragma unroll
+              for (int b = 0; b < 8; ++b)  // (lanes start at different banks)
+                *reinterpret_cast<uint4*>(vr + c * (KB * 128) + ((b + lane) & 7) * 16) =
+                    make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
         }
@@ -876,39 +980,48 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
       tc_fence_after();
       const float inv = lt > 0.0f ? 1.0f / lt : 0.0f;
-      g0 *= inv;
-      g1 *= inv;
       const float lse = lt > 0.0f ? (mm + __log2f(lt)) * 0.69314718055994531f : ninf;
       const bool mine = share || !pc.single || grp == 0;
-      const int c0 = share ? grp * (D / 64) : 0, c1 = share ? c0 + D / 64 : D / 32;
       const int64_t orow = (int64_t)(pc.row0 + tok) * a.pd.H + (int64_t)pc.g * G + rh;
       const int64_t prow = (int64_t)pc.slot * a.slot_rows + (pc.single ? 0 : grp * BM) + r;
       if (mine && active) {
-        const bool use0 = share || (grp == 0 && n0 > 0), use1 = share || (grp == 1 && n1 > 0);
+        const int c0 = share ? grp * (D / 64) : 0, c1 = share ? c0 + D / 64 : D / 32;
+        uint8_t* dst = pc.slot >= 0 ? reinterpret_cast<uint8_t*>(a.opart + prow * D)
+                                    : reinterpret_cast<uint8_t*>(a.O + orow * D);
+        g0 *= inv;
+        g1 *= inv;
 #pragma unroll 1
         for (int c = c0; c < c1; ++c) {
-          uint32_t o0[32], o1[32];
+          uint32_t o0[32];
+          if (share) {
+            uint32_t o1[32];
+            tmem_ld32(tl + C::TO + c * 32, o0);
+            tmem_ld32(tl + C::TO + C::TO_STEP + c * 32, o1);
+            tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o0[e] = o1[e] = 0u;
-          if (use0) tmem_ld32(tl + 256 + c * 32, o0);
-          if (use1) tmem_ld32(tl + 384 + c * 32, o1);
-          tmem_wait_ld();
-          float ov[32];
+            for (int e = 0; e < 32; ++e)
+              o0[e] = __float_as_uint((g0 > 0.0f ? __uint_as_float(o0[e]) * g0 : 0.0f) +
+                                      (g1 > 0.0f ? __uint_as_float(o1[e]) * g1 : 0.0f));
+          } else if (pc.n > 0) {
+            tmem_ld32(tO + c * 32, o0);
+            tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            ov[e] = (use0 && g0 > 0.0f ? __uint_as_float(o0[e]) * g0 : 0.0f) +
-                    (use1 && g1 > 0.0f ? __uint_as_float(o1[e]) * g1 : 0.0f);
+            for (int e = 0; e < 32; ++e)
+              o0[e] = inv > 0.0f ? __float_as_uint(__uint_as_float(o0[e]) * inv) : 0u;
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o0[e] = 0u;
+          }
           if (row_ok && pc.slot >= 0) {
-            uint32_t* dst = reinterpret_cast<uint32_t*>(a.opart + prow * D + c * 32);
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) store8(dst + e, reinterpret_cast<uint32_t*>(ov) + e, true);
+            for (int e = 0; e < 32; e += 8) store8(dst + c * 128 + e * 4, o0 + e, true);
           } else if (row_ok) {
-            uint32_t* dst = reinterpret_cast<uint32_t*>(a.O + orow * D + c * 32);
             uint32_t w[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(ov[2 * e], ov[2 * e + 1]);
-            store8(dst, w, a.wide);
-            store8(dst + 8, w + 8, a.wide);
+            for (int e = 0; e < 16; ++e)
+              w[e] = pack_bf16x2(__uint_as_float(o0[2 * e]), __uint_as_float(o0[2 * e + 1]));
+            store8(dst + c * 64, w, a.wide);
+            store8(dst + c * 64 + 32, w + 8, a.wide);
           }
           __syncwarp();  // the loads from tensor memory are warp-wide
         }
@@ -938,60 +1051,85 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 
 // Merge of the cut items' partial outputs in order: lse = ln sum e^(lse_j), O =
 // sum e^(lse_j - lse) O_j.  The item that CTA c begins has its parts in slots 2 c +
-// 1, 2 c + 2, 2 c + 4, ...  A warp per row, all rows of all cut items dealt out
-// evenly.
+// 1, 2 c + 2, 2 c + 4, ...  All rows of all cut items are dealt out evenly, 8
+// threads to a row, so that a warp has four rows' loads in flight.
 template <int D>
 __global__ void __launch_bounds__(256) k_paged_merge(const __grid_constant__ TcArgs a) {
+  static_assert(kGrid <= 256, "a thread per CTA of the attention");
+  __shared__ int4 rec[kGrid];
+  __shared__ int ends[kGrid];  // rows of the items up to and with c
+  __shared__ int warp_sum[8];
+  const int tid = threadIdx.x, lane = tid & 31;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int lane = threadIdx.x & 31;
-  const int warps = gridDim.x * 8;
-  int row = blockIdx.x * 8 + (threadIdx.x >> 5);  // among the rows still to come
+  int4 r = make_int4(0, 0, 0, 0);
+  if (tid < kGrid) r = a.rec[tid];
+  int inc = r.w > 1 ? r.y * a.pd.G : 0;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(FULL, inc, o);
+    if (lane >= o) inc += x;
+  }
+  if (lane == 31) warp_sum[tid >> 5] = inc;
+  __syncthreads();
+  for (int w = 0; w < tid >> 5; ++w) inc += warp_sum[w];
+  if (tid < kGrid) {
+    rec[tid] = r;
+    ends[tid] = inc;
+  }
+  __syncthreads();
   const float ninf = -__int_as_float(0x7f800000);
-  constexpr int W = D / 32;
-  for (int c0 = 0; c0 < kGrid; c0 += 32) {
-    int mine = 0;
-    if (c0 + lane < kGrid && a.rec[2 * (c0 + lane) + 1].x > 1) mine = a.rec[2 * (c0 + lane)].y * a.pd.G;
-    for (unsigned m = __ballot_sync(FULL, mine > 0); m; m &= m - 1) {
-      const int l = __ffs(m) - 1, rows = __shfl_sync(FULL, mine, l);
-      for (; row < rows; row += warps) {
-        const int4 r0 = a.rec[2 * (c0 + l)];
-        const int parts = a.rec[2 * (c0 + l) + 1].x;
-        const int tok = row / a.pd.G, h = row - tok * a.pd.G;
-        const int tile = tok / a.tpm;  // rows of the second query tile start at BM
-        const int at = tile * BM + (tok - tile * a.tpm) * a.pd.G + h;
-        const int64_t first = 2 * (int64_t)(c0 + l);
-        auto place = [&](int j) { return (first + (j == 0 ? 1 : 2 * j)) * a.slot_rows + at; };
-        float mx = ninf;
-        for (int j = lane; j < parts; j += 32) mx = fmaxf(mx, a.lpart[place(j)]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, o));
-        float acc[W], sw = 0.0f;
-#pragma unroll
-        for (int e = 0; e < W; ++e) acc[e] = 0.0f;
-#pragma unroll 4
-        for (int j = 0; j < parts; ++j) {
-          const float lj = a.lpart[place(j)];
-          const float w = lj == ninf ? 0.0f : __expf(lj - mx);
-          const float* src = a.opart + place(j) * D + lane * W;
-          float v[W];
-          if constexpr (W == 4)
-            *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(src);
-          else
-            *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(src);
-          sw += w;
-#pragma unroll
-          for (int e = 0; e < W; ++e) acc[e] = fmaf(w, v[e], acc[e]);  // (parts that saw nothing hold 0)
-        }
-        const float inv = sw > 0.0f ? 1.0f / sw : 0.0f;
-        const int64_t t = r0.x + tok;
-        const int64_t hq = (int64_t)r0.z * a.pd.G + h;
-        uint32_t* dst = reinterpret_cast<uint32_t*>(a.O + (t * a.pd.H + hq) * D + lane * W);
-#pragma unroll
-        for (int e = 0; e < W / 2; ++e) dst[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-        if (lane == 0) a.lse[hq * a.pd.T + t] = sw > 0.0f ? mx + logf(sw) : ninf;
-      }
-      row -= rows;
+  const int l8 = lane & 7;
+  constexpr int W = D / 8;  // columns per thread
+  const unsigned octet = 0xffu << (lane & 24);
+  for (int row = blockIdx.x * 32 + (tid >> 3); row < ends[kGrid - 1]; row += gridDim.x * 32) {
+    int c = 0, hi = kGrid - 1;  // the first c with ends[c] > row
+    while (c < hi) {
+      const int mid = (c + hi) >> 1;
+      if (ends[mid] > row)
+        hi = mid;
+      else
+        c = mid + 1;
     }
+    r = rec[c];
+    const int in = row - (ends[c] - r.y * a.pd.G);
+    const int tok = in / a.pd.G, h = in - tok * a.pd.G;
+    const int tile = tok / a.tpm;  // rows of the second query tile start at BM
+    const int64_t at = tile * BM + (tok - tile * a.tpm) * a.pd.G + h;
+    auto place = [&](int j) { return (int64_t)(2 * c + (j == 0 ? 1 : 2 * j)) * a.slot_rows + at; };
+    float mx = ninf;
+    for (int j = l8; j < r.w; j += 8) mx = fmaxf(mx, a.lpart[place(j)]);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(octet, mx, o));
+    float acc[W], sw = 0.0f;
+#pragma unroll
+    for (int e = 0; e < W; ++e) acc[e] = 0.0f;
+#pragma unroll 2
+    for (int j = 0; j < r.w; ++j) {
+      const float lj = a.lpart[place(j)];
+      const float4* src = reinterpret_cast<const float4*>(a.opart + place(j) * D + l8 * W);
+      float4 v[W / 4];
+#pragma unroll
+      for (int e = 0; e < W / 4; ++e) v[e] = src[e];
+      const float w = lj == ninf ? 0.0f : __expf(lj - mx);
+      sw += w;
+#pragma unroll
+      for (int e = 0; e < W / 4; ++e) {  // (parts in which a row saw nothing hold zeros)
+        acc[4 * e] = fmaf(w, v[e].x, acc[4 * e]);
+        acc[4 * e + 1] = fmaf(w, v[e].y, acc[4 * e + 1]);
+        acc[4 * e + 2] = fmaf(w, v[e].z, acc[4 * e + 2]);
+        acc[4 * e + 3] = fmaf(w, v[e].w, acc[4 * e + 3]);
+      }
+    }
+    const float inv = sw > 0.0f ? 1.0f / sw : 0.0f;
+    const int64_t t = r.x + tok, hq = (int64_t)r.z * a.pd.G + h;
+    uint4* dst = reinterpret_cast<uint4*>(a.O + (t * a.pd.H + hq) * D + l8 * W);
+#pragma unroll
+    for (int e = 0; e < W / 8; ++e)
+      dst[e] = make_uint4(pack_bf16x2(acc[8 * e] * inv, acc[8 * e + 1] * inv),
+                          pack_bf16x2(acc[8 * e + 2] * inv, acc[8 * e + 3] * inv),
+                          pack_bf16x2(acc[8 * e + 4] * inv, acc[8 * e + 5] * inv),
+                          pack_bf16x2(acc[8 * e + 6] * inv, acc[8 * e + 7] * inv));
+    if (l8 == 0) a.lse[hq * a.pd.T + t] = sw > 0.0f ? mx + logf(sw) : ninf;
   }
 }
 
@@ -1008,7 +1146,7 @@ struct Ws {
 Ws carve(const PagedDims& pd) {
   Ws w;
   const size_t rows = (size_t)kSlots * slot_rows(pd);
-  w.lpart = ((size_t)kGrid * 32 + 255) & ~size_t(255);
+  w.lpart = ((size_t)kGrid * 16 + 255) & ~size_t(255);
   w.opart = w.lpart + ((rows * 4 + 255) & ~size_t(255));
   w.bytes = w.opart + rows * pd.d * 4;
   return w;
