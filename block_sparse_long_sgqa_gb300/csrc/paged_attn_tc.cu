@@ -39,10 +39,10 @@ constexpr int NPC = 4;    // pieces in the ring
 constexpr int NTHREADS = 384;
 constexpr int kGrid = 152;
 
-// The reference maximum may lag behind by this much in the sum of a tile's
-// weights before it is raised: bf16 and fp32 hold such weights with the same
-// relative precision as weights up to 1.
-constexpr float kLazySum = 4096.0f;
+// A tile's maximum may exceed the reference by a factor of 2^kLazy before the
+// reference is raised and O rescaled: bf16 and fp32 hold weights up to 2^kLazy with
+// the same relative precision as weights up to 1.
+constexpr float kLazy = 8.0f;
 
 template <int D>
 struct Cfg {
@@ -230,106 +230,6 @@ __device__ __forceinline__ uint32_t seen_bits(int k, int lo, int hi) {
   return (b >= 32 ? FULL : (1u << b) - 1u) & ~((1u << a) - 1u);
 }
 
-// A tile in two passes: its masked maximum, then the weights; raises the
-// reference maximum and rescales what was accumulated under the old one.
-// S is 128 columns at tS, P 64 at tP (which may be the first of S's).  Returns the
-// maximum and the sum.
-template <int D>
-__device__ __noinline__ float2 tile_two_pass(uint32_t tS, uint32_t tP, uint32_t tO, float sl2, uint32_t a0,
-                                             uint32_t a1, uint32_t a2, uint32_t a3, bool have_o,
-                                             float m_used, float l) {
-  const float ninf = -__int_as_float(0x7f800000);
-  float mx[4] = {ninf, ninf, ninf, ninf};
-  uint32_t v[64];
-#pragma unroll 1
-  for (int h = 0; h < 2; ++h) {
-    tmem_ld32(tS + h * 64, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
-    tmem_ld32(tS + h * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
-    tmem_wait_ld();
-    const uint32_t am0 = h == 0 ? a0 : a2, am1 = h == 0 ? a1 : a3;
-#pragma unroll
-    for (int e = 0; e < 32; ++e) {
-      mx[e & 1] = fmaxf(mx[e & 1], ((am0 >> e) & 1u) ? __uint_as_float(v[e]) : ninf);
-      mx[2 + (e & 1)] = fmaxf(mx[2 + (e & 1)], ((am1 >> e) & 1u) ? __uint_as_float(v[32 + e]) : ninf);
-    }
-  }
-  const float smax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
-  const bool raise = smax > m_used;
-  const float f = raise ? ex2(m_used - smax) : 1.0f;  // 0 for the first keys a row sees
-  if (have_o && __any_sync(FULL, raise)) {
-#pragma unroll 1
-    for (int c = 0; c < D / 32; ++c) {
-      uint32_t o[32];
-      tmem_ld32(tO + c * 32, o);
-      tmem_wait_ld();
-#pragma unroll
-      for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-      tmem_st32(tO + c * 32, o);
-    }
-  }
-  l *= f;
-  if (raise) m_used = smax;
-  const float msub = m_used == ninf ? 0.0f : m_used;
-  float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 1
-  for (int h = 0; h < 2; ++h) {
-    uint32_t pk[32];
-    tmem_ld32(tS + h * 64, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
-    tmem_ld32(tS + h * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
-    tmem_wait_ld();
-    const uint32_t am0 = h == 0 ? a0 : a2, am1 = h == 0 ? a1 : a3;
-#pragma unroll
-    for (int e = 0; e < 64; e += 2) {
-      const uint32_t am = e < 32 ? am0 : am1;
-      const float x0 = fmaf(__uint_as_float(v[e]), sl2, -msub);
-      const float x1 = fmaf(__uint_as_float(v[e + 1]), sl2, -msub);
-      const float p0 = ex2(((am >> (e & 31)) & 1u) ? x0 : ninf);
-      const float p1 = ex2(((am >> ((e & 31) + 1)) & 1u) ? x1 : ninf);
-      sum[e & 2] += p0;
-      sum[(e & 2) + 1] += p1;
-      pk[e >> 1] = pack_bf16x2(p0, p1);
-    }
-    tmem_st32(tP + h * 32, pk);  // (over S values that have been read)
-  }
-  return make_float2(m_used, l + ((sum[0] + sum[1]) + (sum[2] + sum[3])));
-}
-
-// The weights of a tile under the reference maximum -nm, packed, and their sum
-// (two packed sums of two).  MASK: am holds a bit for each key the row sees.
-// after_read: called once S is in registers.
-template <bool MASK, typename F>
-__device__ __forceinline__ float tile_weights(uint32_t tS, uint64_t sl2x2, float nm,
-                                              const uint32_t (&am)[4], uint32_t (&pk)[64],
-                                              F after_read) {
-  const float ninf = -__int_as_float(0x7f800000);
-  const uint64_t nm2 = f2_pack(nm, nm);
-  uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t v[64];
-    tmem_ld32(tS + h * 64, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
-    tmem_ld32(tS + h * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
-    tmem_wait_ld();
-    if (h == 1) after_read();
-#pragma unroll
-    for (int e = 0; e < 64; e += 2) {
-      float x0, x1;
-      f2_unpack(f2_fma(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), sl2x2, nm2), x0, x1);
-      if constexpr (MASK) {  // by selection: S of keys outside the cache may be NaN
-        const uint32_t m = am[2 * h + (e >> 5)];
-        x0 = ((m >> (e & 31)) & 1u) ? x0 : ninf;
-        x1 = ((m >> ((e & 31) + 1)) & 1u) ? x1 : ninf;
-      }
-      const float p0 = ex2(x0), p1 = ex2(x1);
-      acc[(e >> 1) & 3] = f2_add(acc[(e >> 1) & 3], f2_pack(p0, p1));
-      pk[h * 32 + (e >> 1)] = pack_bf16x2(p0, p1);
-    }
-  }
-  float s0, s1;
-  f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), s0, s1);
-  return s0 + s1;
-}
-
 // 8 consecutive 32-bit words of one row
 __device__ __forceinline__ void store8(void* p, const uint32_t* w, bool wide) {
   if (wide) {
@@ -449,7 +349,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   // The others sleep until the first piece is there: waiting on its barrier they
   // slowed the walk of warp 0 from 2 to 12 thousand cycles.
   if (warp != 0) asm volatile("bar.sync 1, 384;" ::: "memory");
-
+  // Registers: a softmax thread holds a row's 128 scores.  2 x 128 x kRegsMore +
+  // 128 x kRegsLess stays within the 384 x 168 of the launch.
+  constexpr int kRegsLess = 80, kRegsMore = 208;
+  static_assert(256 * kRegsMore + 128 * kRegsLess <= NTHREADS * 168, "the launch's registers");
+  if (warp < 4) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLess));
   if (warp == 0) {
     // ============================================================ pieces, Q
     if (lane == 0) tma_prefetch_desc(&mq);
@@ -508,7 +413,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         return true;
       }
       if (idle == 0) t_prog = globaltimer();
-      __nanosleep(64);
+      __nanosleep(500);
       if ((++idle & 63) != 0) return true;
       int stop = 0;
       if (lane == 0) {
@@ -702,7 +607,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const int uses = cnt / NS + (k < cnt % NS ? 1 : 0);
         if (uses > 0) mbar_wait_drain(&full[k], (uint32_t)((uses - 1) & 1), a.status, isK ? 392 : 393);
       }
-  } else if (warp == 3) {
+  } else {
     // ============================================================== products
     // The whole warp walks the loop and one elected lane issues, so that the
     // loop's state and the operand descriptors stay in uniform registers: with
@@ -722,6 +627,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     int ks = 0, vs = 0;             // slots of the next key tile
     uint32_t kph = 0, vph = 0;      // and their phases
     uint32_t pph = 0, sph = 0;      // phases of p_full and s_empty, bit = group
+    uint32_t used = 0;              // groups that have had an S
     int qs = 0;                     // query slot of the next single tile
     uint32_t qph = 0;               // phases of q_full, bit = slot
     bool first = true, ok = true;
@@ -750,8 +656,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       const int J = n << sh;
       const int slot = single ? qs : 0;  // of the first query tile
       // S of step j: group j & 1, query tile j & sh, the next key tile when j & sh is 0
-      auto do_qk = [&](int j) -> bool {
-        if ((j & sh) == 0 && !warp_poll(&k_full[ks], kph, ab, a.status, 337)) return false;
+      auto qk = [&](int j) {
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)(j & 1) * 128;
         const uint32_t la = lq + (uint32_t)(slot + (j & sh)) * (C::TILE / 16), lb = lk + (uint32_t)ks * (C::TILE / 16);
@@ -770,21 +675,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           ks = 0;
           kph ^= 1;
         }
-        return true;
       };
-      ok = J == 0 || (do_qk(0) && (J < 2 || do_qk(1)));
-      for (int j = 0; ok && j < J; ++j) {
+      // O of group j & 1 += P V
+      auto pv = [&](int j) {
         const int grp = j & 1;
-        if constexpr (C::OWN_P) {  // the next S as soon as this one has been read
-          ok = warp_poll(&s_empty[grp], (sph >> grp) & 1u, ab, a.status, 347);
-          sph ^= 1u << grp;
-          if (ok && j + 2 < J) ok = do_qk(j + 2);
-          if (!ok) break;
-        }
-        ok = ((j & sh) != 0 || warp_poll(&v_full[vs], vph, ab, a.status, 338)) &&
-             warp_poll(&p_full[grp], (pph >> grp) & 1u, ab, a.status, 339);
-        if (!ok) break;
-        pph ^= 1u << grp;
         tc_fence_after();
         const uint32_t d = tmem + C::TO + (uint32_t)grp * C::TO_STEP;
         const uint32_t pa = tmem + C::TP + (uint32_t)grp * C::TP_STEP;
@@ -803,10 +697,69 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           vs = 0;
           vph ^= 1;
         }
-        // products of one thread run in issue order, so this S overwrites P
-        // only after the product above has read it
-        if constexpr (!C::OWN_P) {
-          if (j + 2 < J) ok = do_qk(j + 2);
+      };
+      if constexpr (C::OWN_P) {
+        // Both products as soon as what they need is there, each kind in step order
+        int nqk = 0, npv = 0;
+        uint64_t t_prog = 0;
+        uint32_t idle = 0;
+        while (npv < J) {
+          bool progress = false;
+          if (nqk < J) {
+            const int g = nqk & 1;
+            if (__all_sync(FULL, ((used >> g & 1u) == 0u || mbar_test(&s_empty[g], (sph >> g) & 1u)) &&
+                                     ((nqk & sh) != 0 || mbar_test(&k_full[ks], kph)))) {
+              if (used >> g & 1u) sph ^= 1u << g;
+              used |= 1u << g;
+              qk(nqk++);
+              progress = true;
+            }
+          }
+          if (npv < nqk) {
+            const int g = npv & 1;
+            if (__all_sync(FULL, mbar_test(&p_full[g], (pph >> g) & 1u) &&
+                                     ((npv & sh) != 0 || mbar_test(&v_full[vs], vph)))) {
+              pph ^= 1u << g;
+              pv(npv++);
+              progress = true;
+            }
+          }
+          if (progress) {
+            idle = 0;
+          } else {
+            if (idle == 0) t_prog = globaltimer();
+            if ((++idle & 255) == 0) {
+              int stop = 0;
+              if (ab.set()) {
+                stop = 1;
+              } else if (globaltimer() - t_prog > kWaitLimitNs) {
+                if (lane == 0) ab.raise(a.status, 337);
+                stop = 1;
+              }
+              if (__any_sync(FULL, stop)) {
+                ok = false;
+                break;
+              }
+            }
+          }
+        }
+      } else {
+        auto qk_when = [&](int j) -> bool {
+          if ((j & sh) == 0 && !warp_poll(&k_full[ks], kph, ab, a.status, 337)) return false;
+          qk(j);
+          return true;
+        };
+        ok = J == 0 || (qk_when(0) && (J < 2 || qk_when(1)));
+        for (int j = 0; ok && j < J; ++j) {
+          const int g = j & 1;
+          ok = ((j & sh) != 0 || warp_poll(&v_full[vs], vph, ab, a.status, 338)) &&
+               warp_poll(&p_full[g], (pph >> g) & 1u, ab, a.status, 339);
+          if (!ok) break;
+          pph ^= 1u << g;
+          pv(j);
+          // products of one thread run in issue order, so this S overwrites P
+          // only after the product above has read it
+          if (j + 2 < J) ok = qk_when(j + 2);
         }
       }
       if (single && n > 0) qs ^= 1;
@@ -816,7 +769,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       mbar_wait_drain(mma_done, 0, a.status, 399);
     }
     __syncwarp();
+  }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMore));
     // =============================================================== softmax
     const int grp = (warp - 4) >> 2, quad = warp & 3;
     const int r = quad * 32 + lane;
@@ -851,81 +806,95 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         ++sc;
         tc_fence_after();
         const int k0 = (pc.tb + t) * KB;
-        // S has been read: with its own P, the next one may be computed
-        auto s_read = [&]() {
-          if constexpr (C::OWN_P) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s_empty[grp]);
-          }
-        };
-        // ... and P may be written once the last product with it is done
+        // P may be written, and O rescaled, once the last product with them is done
+        // (without its own P, S was computed behind that product)
         auto p_free = [&]() -> bool {
           if constexpr (C::OWN_P) {
-            if (sc == 1) return true;
-            return __all_sync(FULL, mbar_wait(&p_empty[grp], (uint32_t)(sc & 1), ab, a.status, 348));
+            if (sc > 1)
+              return __all_sync(FULL, mbar_wait(&p_empty[grp], (uint32_t)(sc & 1), ab, a.status, 348));
           }
           return true;
         };
+        uint32_t v[128];
         if (active) {
-          const bool whole = __all_sync(FULL, lo <= k0 && k0 + KB <= hi);
-          uint32_t am[4] = {FULL, FULL, FULL, FULL};
-          if (!whole) {
 #pragma unroll
-            for (int w = 0; w < 4; ++w) am[w] = seen_bits(k0 + 32 * w, lo, hi);
-          }
-          const bool none = !row_ok || (am[0] | am[1] | am[2] | am[3]) == 0u;
-          // A row's first keys: the reference is the maximum of 32 of them (of the
-          // tile's end where a window begins in it); the sum below shows whether
-          // the others exceed it by much.
-          if (__any_sync(FULL, m_used == ninf && !none)) {
-            const int c = pc.lo > k0 ? 3 : 0;
-            uint32_t v[32];
-            tmem_ld32(tS + c * 32, v);
-            tmem_wait_ld();
-            float mx[4] = {ninf, ninf, ninf, ninf};
-            const uint32_t m = c == 0 ? am[0] : am[3];
+          for (int w = 0; w < 4; ++w)
+            tmem_ld32(tS + w * 32, *reinterpret_cast<uint32_t(*)[32]>(&v[w * 32]));
+          tmem_wait_ld();
+        }
+        if constexpr (C::OWN_P) {  // S is in registers: the next one may be computed
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_empty[grp]);
+        }
+        if (active) {
+          if (!__all_sync(FULL, lo <= k0 && k0 + KB <= hi)) {
+            // by selection: S of keys outside the cache may be NaN
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              mx[e & 3] = fmaxf(mx[e & 3], ((m >> e) & 1u) ? __uint_as_float(v[e]) : ninf);
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
-            if (m_used == ninf) m_used = top;
-          }
-          bool fast = __all_sync(FULL, m_used != ninf || none);
-          const float nm = m_used == ninf ? 0.0f : -m_used;
-          bool read = false;
-          if (fast) {
-            // One pass under the reference maximum; P is written only if the
-            // tile's weights sum to at most kLazySum in every row.
-            uint32_t pk[64];
-            float sum;
-            auto keep = [&]() {};
-            if (whole)
-              sum = tile_weights<false>(tS, sl2x2, nm, am, pk, keep);
-            else
-              sum = tile_weights<true>(tS, sl2x2, nm, am, pk, keep);
-            fast = __all_sync(FULL, sum <= kLazySum || !row_ok);
-            if (fast) {
-              s_read();
-              read = true;
-              ok = p_free();
-              if (!ok) break;
-              tmem_st32(tP, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
-              tmem_st32(tP + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
-              l += sum;
+            for (int w = 0; w < 4; ++w) {
+              const uint32_t m = seen_bits(k0 + 32 * w, lo, hi);
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                v[w * 32 + e] = ((m >> e) & 1u) ? v[w * 32 + e] : __float_as_uint(ninf);
             }
           }
-          if (!fast) {
-            ok = p_free();
-            if (!ok) break;
-            const float2 ml =
-                tile_two_pass<D>(tS, tP, tO, sl2, am[0], am[1], am[2], am[3], t > t0, m_used, l);
-            m_used = ml.x;
-            l = ml.y;
+          float mx[4] = {ninf, ninf, ninf, ninf};
+#pragma unroll
+          for (int e = 0; e < 128; e += 8) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              mx[c] = fmaxf(fmaxf(mx[c], __uint_as_float(v[e + 2 * c])), __uint_as_float(v[e + 2 * c + 1]));
           }
-          if (!read) s_read();
+          const float smax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+          const bool raise = smax > m_used + kLazy;
+          if (__any_sync(FULL, raise)) {
+            const float f = raise ? ex2(m_used - smax) : 1.0f;  // 0 for the first keys a row sees
+            if (t > t0) {
+              ok = p_free();
+              if (!ok) break;
+#pragma unroll 1
+              for (int c = 0; c < D / 8; ++c) {
+                uint32_t o[8];
+                tmem_ld8(tO + c * 8, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st8(tO + c * 8, o);
+              }
+            }
+            l *= f;
+            if (raise) m_used = smax;
+          }
+          const float nm = m_used == ninf ? 0.0f : -m_used;
+          const uint64_t nm2 = f2_pack(nm, nm);
+          uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int e = 0; e < 64; e += 2) {
+              float x0, x1;
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(v[h * 64 + e]), __uint_as_float(v[h * 64 + e + 1])),
+                               sl2x2, nm2), x0, x1);
+              const float p0 = ex2(x0), p1 = ex2(x1);
+              acc[(e >> 1) & 3] = f2_add(acc[(e >> 1) & 3], f2_pack(p0, p1));
+              pk[e >> 1] = pack_bf16x2(p0, p1);
+            }
+            if (h == 0) {
+              ok = p_free();
+              if (!ok) break;
+            }
+            tmem_st32(tP + h * 32, pk);
+          }
+          if (!ok) break;
+          float s0, s1;
+          f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), s0, s1);
+          l += s0 + s1;
         } else {
-          s_read();
+          // (a warp without rows must not run ahead: its next arrival on p_full
+          // would count for this tile)
+          ok = p_free();
+          if (!ok) break;
         }
         // Rows of V that no row of the item sees are zeroed before the product:
         // they may hold anything, and 0 times an infinity or NaN would count.
