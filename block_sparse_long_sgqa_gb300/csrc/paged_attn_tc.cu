@@ -101,6 +101,12 @@ constexpr int kWtSingle = 2, kWtDouble = 3;
 constexpr int kOver = 3;
 // Shortest range of a CTA, in line units: two key tiles of a single query tile.
 constexpr int64_t kLeastShare = 2 * KB * kWtSingle;
+// Small calls: items of up to kWhole key tiles are not cut at all, longer ones into
+// parts of kPart tiles, when that makes no more pieces than there are CTAs.  Each
+// piece is then one CTA's range, kSlotLen long.  (A cut costs its merge, about
+// 4 us; a CTA takes 0.6 us a tile.)
+constexpr int kWhole = 8, kPart = 6;
+constexpr int64_t kSlotLen = int64_t(1) << 20;
 // A range that ends within kSnap tiles of an item's beginning or end leaves the
 // item whole, when ranges are long enough for that to leave no part empty.
 constexpr int kSnap = 2;
@@ -114,10 +120,22 @@ struct Cut {
   int q0, ql, kv;
   int ipt, items;
   int tw;               // a key tile on the line
+  int tiles;            // most key tiles of an item
   int64_t A, B, head;   // head: all items of a KV group
 };
+// Pieces of each of the request's items in a small call.
+__device__ __forceinline__ int parts_of(const Cut& c) {
+  return c.tiles <= kWhole ? 1 : (int)((unsigned)(c.tiles + kPart - 1) / (unsigned)kPart);
+}
+__device__ __forceinline__ void cut_small(Cut& c) {
+  const int parts = parts_of(c);
+  c.A = parts * kSlotLen;
+  c.B = 0;
+  c.head = c.A * c.items;
+  c.tw = c.tiles > 1 ? (int)((unsigned)c.A / (unsigned)c.tiles) : (int)kSlotLen;
+}
 __device__ __forceinline__ Cut cut_of(const TcArgs& a, int s, bool tell) {
-  Cut c{0, 0, 0, 1, 0, 0, 0, 0, 0};
+  Cut c{0, 0, 0, 1, 0, 0, 0, 0, 0, 0};
   if (s >= a.pd.N) return c;
   const SeqLen q = seq_len_of(a.pd, a.q_start, a.kv_len, s, a.status, tell);
   c.q0 = q.q0;
@@ -136,6 +154,8 @@ __device__ __forceinline__ Cut cut_of(const TcArgs& a, int s, bool tell) {
     keys = q.kv - q.ql + c.ipt;
     slope = c.ipt;
   }
+  // (a window's first key may lie anywhere in its tile)
+  c.tiles = a.pd.window > 0 ? min((keys + KB - 1) / KB + 1, (q.kv + KB - 1) / KB) : (q.kv + KB - 1) / KB;
   c.A = (int64_t)(keys + kOver * KB) * wt;
   c.B = (int64_t)slope * wt;
   c.head = c.A * c.items + c.B * ((int64_t)c.items * (c.items - 1) / 2);
@@ -309,17 +329,19 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     fence_mbar_init();
   }
   if (warp == 3) tmem_alloc(tmem_slot, 512);
+  if (lane == 0 && warp >= 1 && warp <= 3) tma_prefetch_desc(warp == 1 ? &mk : warp == 2 ? &mv : &mq);
 
   // ---- the line: its length, the part of it that waves would take, and the keys
   // that several items share.  Exact integer sums, the same in every CTA.
-  int64_t* sums = reinterpret_cast<int64_t*>(xmax);  // [warp][3]
+  int64_t* sums = reinterpret_cast<int64_t*>(xmax);  // [warp][4]
   const unsigned grid = gridDim.x;
   Cut cut = cut_of(a, threadIdx.x, blockIdx.x == 0);  // (warp 0 keeps its 32)
   {
-    int64_t line = 0, wave = 0, keys = 0;
+    int64_t line = 0, wave = 0, keys = 0, parts = 0;
     for (int s = threadIdx.x; s < a.pd.N; s += NTHREADS) {
       const Cut c = s < NTHREADS ? cut : cut_of(a, s, blockIdx.x == 0);
       line += c.head * a.pd.Hkv;
+      parts += (int64_t)parts_of(c) * c.items * a.pd.Hkv;
       if (c.items > 1 && a.pd.window == 0) {
         const unsigned all = (unsigned)c.items * (unsigned)a.pd.Hkv, in = all - all % grid;
         const unsigned g = in / (unsigned)c.items;
@@ -333,12 +355,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         line += __shfl_xor_sync(FULL, line, o);
         wave += __shfl_xor_sync(FULL, wave, o);
         keys += __shfl_xor_sync(FULL, keys, o);
+        parts += __shfl_xor_sync(FULL, parts, o);
       }
     }
     if (lane == 0) {
-      sums[warp * 3] = line;
-      sums[warp * 3 + 1] = wave;
-      sums[warp * 3 + 2] = keys;
+      sums[warp * 4] = line;
+      sums[warp * 4 + 1] = wave;
+      sums[warp * 4 + 2] = keys;
+      sums[warp * 4 + 3] = parts;
     }
   }
   tc_fence_before();
@@ -357,17 +381,22 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLess));
   if (warp == 0) {
     // ============================================================ pieces, Q
-    if (lane == 0) tma_prefetch_desc(&mq);
-    int64_t line = 0, in_waves = 0, keys = 0;
+    int64_t line = 0, in_waves = 0, keys = 0, parts = 0;
     for (int i = 0; i < NTHREADS / 32 && i * 32 < a.pd.N; ++i) {
-      line += sums[i * 3];
-      in_waves += sums[i * 3 + 1];
-      keys += sums[i * 3 + 2];
+      line += sums[i * 4];
+      in_waves += sums[i * 4 + 1];
+      keys += sums[i * 4 + 2];
+      parts += sums[i * 4 + 3];
     }
     const bool waves = keys * a.pd.Hkv * (4 * D) > kWaveBytes;
-    const int64_t total = line - (waves ? in_waves : 0);
+    const bool small = parts <= (int64_t)grid && !waves;
+    const int64_t total = small ? parts * kSlotLen : line - (waves ? in_waves : 0);
     int64_t share = (total + grid - 1) / grid;
     if (share < kLeastShare) share = kLeastShare;
+    if (small) {
+      share = kSlotLen;
+      if (cut.items > 0) cut_small(cut);
+    }
     int pub = 0, nq = 0;     // pieces published, their Q looked after
     int qs = 0;              // query slot of the next single tile
     uint32_t qph = 3u;       // phases of q_empty to wait for, bit = slot
@@ -449,7 +478,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     bool ok = true;
     int held = 0;  // the 32 requests this warp's lanes hold
     auto hold = [&](int s0) {
-      if (held != s0) cut = cut_of(a, s0 + lane, false);
+      if (held != s0) {
+        cut = cut_of(a, s0 + lane, false);
+        if (small && cut.items > 0) cut_small(cut);
+      }
       held = s0;
     };
     // items that go in waves, all KV groups of a request together
@@ -520,7 +552,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             if (x <= at) return 0;
             if (x - at >= cost) return n;
             const int t = (int)min((unsigned)n, ((unsigned)(x - at) + tw - 1) / tw);
-            return share < kSnapShare ? t : t <= kSnap ? 0 : t >= n - kSnap ? n : t;
+            return share < kSnapShare || small ? t : t <= kSnap ? 0 : t >= n - kSnap ? n : t;
           };
           const int t0 = tiles_before(from), t1 = tiles_before(to);
           if (n == 0 ? at >= from : t1 > t0) {
@@ -563,7 +595,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     uint64_t* empty = isK ? k_empty : v_empty;
     const int NS = isK ? C::SK : C::SV;
     uint8_t* slots = smem + (isK ? C::OFF_K : C::OFF_V);
-    if (lane == 0) tma_prefetch_desc(map);
     const int rows_total = a.pd.n_pages * a.pd.Hkv * a.pd.ps;
     const int nbox = KB / a.box;
     int cnt = 0;  // tiles loaded
@@ -801,11 +832,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       const int step = pc.single ? 2 : 1;
       const int t0 = pc.single ? grp : 0;
       for (int t = t0; t < pc.n; t += step) {
+        const int k0 = (pc.tb + t) * KB;
         ok = __all_sync(FULL, mbar_wait(&s_full[grp], (uint32_t)(sc & 1), ab, a.status, 341));
         if (!ok) break;
         ++sc;
         tc_fence_after();
-        const int k0 = (pc.tb + t) * KB;
         // P may be written, and O rescaled, once the last product with them is done
         // (without its own P, S was computed behind that product)
         auto p_free = [&]() -> bool {
@@ -896,8 +927,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           ok = p_free();
           if (!ok) break;
         }
-        // Rows of V that no row of the item sees are zeroed before the product:
-        // they may hold anything, and 0 times an infinity or NaN would count.
+        // Rows of V that no row of the item sees are zeroed before the product: they
+        // may hold anything, and 0 times an infinity or NaN would count.  (Not before
+        // S is there: only then has the slot's last tile been used.)
         if ((pc.single || grp == 0) && (pc.lo > k0 || pc.hi < k0 + KB)) {
           const int vt = vbase + t, vs = vt % C::SV;
           ok = __all_sync(FULL, mbar_wait(&v_full[vs], (uint32_t)((vt / C::SV) & 1), ab, a.status, 342));
