@@ -7,37 +7,26 @@
 //
 // A query tile is 128 / G tokens with their G query heads as the M = 128 rows of
 // every product, so each K and V tile that is read serves the whole KV group.
-// An item is up to two query tiles of a (request, KV group); one CTA per SM.
-// Requests with one query tile (single tokens, drafts) let the two softmax
-// groups take alternate key tiles; longer ones give each group its own query
-// tile, and each key tile serves both.
-//
-// Who does what follows from the lengths alone.  All items lie one after
-// another on a line, each as long as its work; the line is cut into one equal
-// range per CTA, and a key tile belongs to the CTA whose range holds its place.
-// An item cut by a range's end leaves partial outputs, which a second kernel
-// merges in order.  That balances any mix of lengths to a tile, but the CTAs
-// then read different keys at any one time.  When the keys that several items
-// share exceed what L2 holds, full waves of whole items come first: item w
-// grid + c goes to CTA c, so that neighbours read the same keys together, and
-// only the rest of each request's items goes on the line.
+// paged_line.cuh lays the work out over one CTA per SM, in items of up to two query
+// tiles.  Requests with one query tile (single tokens, drafts) let the two softmax
+// groups take alternate key tiles; longer ones give each group its own query tile,
+// and each key tile serves both.
 //
 // Roles (12 warps): 0 walks this CTA's pieces, publishes them in a ring and
 // loads Q; 1 and 2 load K and V tiles through the page table (TMA boxes of
 // gcd(page size, 128) rows, one lane each); 3 issues the products; 4-7 and 8-11
 // are the softmax groups, one thread per row, and write the outputs.  All rings
 // run on across pieces, so the next piece's keys load during the current one.
-#include "paged.h"
+#include "paged_line.cuh"
 
 namespace sgqa {
 namespace {
 
-constexpr unsigned FULL = 0xffffffffu;
 constexpr int BM = 128;   // rows of a query tile
 constexpr int KB = 128;   // keys of a tile
 constexpr int NPC = 4;    // pieces in the ring
 constexpr int NTHREADS = 384;
-constexpr int kGrid = 152;
+constexpr int kGrid = 152;  // one CTA per SM
 
 // A tile's maximum may exceed the reference by a factor of 2^kLazy before the
 // reference is raised and O rescaled: bf16 and fp32 hold weights up to 2^kLazy with
@@ -66,134 +55,15 @@ struct Cfg {
   static_assert(SMEM <= 232448, "shared memory of one CTA");
 };
 
-struct TcArgs {
-  PagedDims pd;
-  const int32_t *page_table, *q_start, *kv_len;
+struct TcArgs : LineArgs {
   __nv_bfloat16* O;
   float* lse;
-  float *opart, *lpart;  // partial outputs [slot][slot_rows][D], their lse [slot][slot_rows]
-  int4* rec;             // [kGrid]: row0, tokens, group and parts of the item that CTA c
-                         // begins and another ends
-  int32_t* status;
-  int slot_rows;
   int box;               // rows of a K/V box: gcd(page size, 128)
-  int tpm;               // tokens of a query tile
   int wide;              // O is 32-byte aligned
   float sl2;             // scale * log2(e)
 };
 
-struct Piece {
-  int s, g, row0, ntok;  // request, KV group, first token row, tokens
-  int pos0;              // position of the first token
-  int tb, n;             // first key tile, key tiles
-  int lo, hi;            // keys that some row of the item sees
-  int single;            // one query tile, key tiles alternate between the groups
-  int slot;              // partial output (-1: the piece is the whole item)
-  int end;               // no further piece
-};
 static_assert(sizeof(Piece) <= 64, "ring slot");
-
-// Lengths on the line, in keys times a weight: a key tile takes kWt[..] * 128
-// (two query tiles cost about half as much again as one), an item kOver tiles
-// more for its beginning and end.  kOver >= 2 also keeps every tile's place
-// inside its item (an item's first and last tile may reach past its keys).
-constexpr int kWtSingle = 2, kWtDouble = 3;
-constexpr int kOver = 3;
-// Shortest range of a CTA, in line units: two key tiles of a single query tile.
-constexpr int64_t kLeastShare = 2 * KB * kWtSingle;
-// Small calls: items of up to kWhole key tiles are not cut at all, longer ones into
-// parts of kPart tiles, when that makes no more pieces than there are CTAs.  Each
-// piece is then one CTA's range, kSlotLen long.  (A cut costs its merge, about
-// 4 us; a CTA takes 0.6 us a tile.)
-constexpr int kWhole = 8, kPart = 6;
-constexpr int64_t kSlotLen = int64_t(1) << 20;
-// A range that ends within kSnap tiles of an item's beginning or end leaves the
-// item whole, when ranges are long enough for that to leave no part empty.
-constexpr int kSnap = 2;
-constexpr int64_t kSnapShare = (int64_t)8 * KB * kWtDouble;
-// K and V bytes of the requests with several items above which waves are used:
-// about half of L2.
-constexpr int64_t kWaveBytes = int64_t(64) << 20;
-
-// How a request is cut: items per KV group, item k taking A + B k on the line.
-struct Cut {
-  int q0, ql, kv;
-  int ipt, items;
-  int tw;               // a key tile on the line
-  int tiles;            // most key tiles of an item
-  int64_t A, B, head;   // head: all items of a KV group
-};
-// Pieces of each of the request's items in a small call.
-__device__ __forceinline__ int parts_of(const Cut& c) {
-  return c.tiles <= kWhole ? 1 : (int)((unsigned)(c.tiles + kPart - 1) / (unsigned)kPart);
-}
-__device__ __forceinline__ void cut_small(Cut& c) {
-  const int parts = parts_of(c);
-  c.A = parts * kSlotLen;
-  c.B = 0;
-  c.head = c.A * c.items;
-  c.tw = c.tiles > 1 ? (int)((unsigned)c.A / (unsigned)c.tiles) : (int)kSlotLen;
-}
-__device__ __forceinline__ Cut cut_of(const TcArgs& a, int s, bool tell) {
-  Cut c{0, 0, 0, 1, 0, 0, 0, 0, 0, 0};
-  if (s >= a.pd.N) return c;
-  const SeqLen q = seq_len_of(a.pd, a.q_start, a.kv_len, s, a.status, tell);
-  c.q0 = q.q0;
-  c.ql = q.ql;
-  c.kv = q.kv;
-  const bool one = q.ql <= a.tpm;
-  const int wt = one ? kWtSingle : kWtDouble;
-  c.ipt = one ? a.tpm : 2 * a.tpm;
-  c.items = one ? (q.ql > 0) : (int)((unsigned)(q.ql + c.ipt - 1) / (unsigned)c.ipt);
-  c.tw = wt * KB;
-  // keys an item sees, at most
-  int keys = q.kv, slope = 0;
-  if (a.pd.window > 0) {
-    keys = min(q.kv, a.pd.window + c.ipt - 1);
-  } else if (a.pd.causal && q.kv >= q.ql) {
-    keys = q.kv - q.ql + c.ipt;
-    slope = c.ipt;
-  }
-  // (a window's first key may lie anywhere in its tile)
-  c.tiles = a.pd.window > 0 ? min((keys + KB - 1) / KB + 1, (q.kv + KB - 1) / KB) : (q.kv + KB - 1) / KB;
-  c.A = (int64_t)(keys + kOver * KB) * wt;
-  c.B = (int64_t)slope * wt;
-  c.head = c.A * c.items + c.B * ((int64_t)c.items * (c.items - 1) / 2);
-  return c;
-}
-// Where item k of a KV group begins, from the group's beginning.
-__device__ __forceinline__ int64_t item_at(int64_t A, int64_t B, int k) {
-  return A * k + B * ((int64_t)k * (k - 1) / 2);
-}
-
-// Item k of group g of request s as one piece (warp-uniform arguments).
-__device__ __forceinline__ Piece item_piece(const TcArgs& a, int s, int q0, int ql, int kv, int ipt,
-                                            int g, int k) {
-  Piece pc;
-  pc.s = s;
-  pc.g = g;
-  pc.row0 = q0 + k * ipt;
-  pc.ntok = min(ipt, ql - k * ipt);
-  pc.pos0 = kv - ql + k * ipt;
-  pc.hi = a.pd.causal ? max(0, min(kv, pc.pos0 + pc.ntok)) : kv;
-  pc.lo = a.pd.window ? max(0, pc.pos0 + 1 - a.pd.window) : 0;
-  pc.tb = pc.lo / KB;
-  pc.n = pc.hi > pc.lo ? (pc.hi + KB - 1) / KB - pc.tb : 0;
-  pc.single = pc.ntok <= a.tpm;
-  pc.slot = -1;
-  pc.end = 0;
-  return pc;
-}
-
-__device__ __forceinline__ int64_t lane_scan(int64_t v) {
-  const int lane = lane_id();
-#pragma unroll 1
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t x = __shfl_up_sync(FULL, v, o);
-    if (lane >= o) v += x;
-  }
-  return v;
-}
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -333,38 +203,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 
   // ---- the line: its length, the part of it that waves would take, and the keys
   // that several items share.  Exact integer sums, the same in every CTA.
-  int64_t* sums = reinterpret_cast<int64_t*>(xmax);  // [warp][4]
-  const unsigned grid = gridDim.x;
-  Cut cut = cut_of(a, threadIdx.x, blockIdx.x == 0);  // (warp 0 keeps its 32)
-  {
-    int64_t line = 0, wave = 0, keys = 0, parts = 0;
-    for (int s = threadIdx.x; s < a.pd.N; s += NTHREADS) {
-      const Cut c = s < NTHREADS ? cut : cut_of(a, s, blockIdx.x == 0);
-      line += c.head * a.pd.Hkv;
-      parts += (int64_t)parts_of(c) * c.items * a.pd.Hkv;
-      if (c.items > 1 && a.pd.window == 0) {
-        const unsigned all = (unsigned)c.items * (unsigned)a.pd.Hkv, in = all - all % grid;
-        const unsigned g = in / (unsigned)c.items;
-        wave += c.head * g + item_at(c.A, c.B, (int)(in - g * c.items));
-        keys += c.kv;
-      }
-    }
-    if (warp * 32 < a.pd.N) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        line += __shfl_xor_sync(FULL, line, o);
-        wave += __shfl_xor_sync(FULL, wave, o);
-        keys += __shfl_xor_sync(FULL, keys, o);
-        parts += __shfl_xor_sync(FULL, parts, o);
-      }
-    }
-    if (lane == 0) {
-      sums[warp * 4] = line;
-      sums[warp * 4 + 1] = wave;
-      sums[warp * 4 + 2] = keys;
-      sums[warp * 4 + 3] = parts;
-    }
-  }
+  int64_t(*warp_sums)[4] = reinterpret_cast<int64_t(*)[4]>(xmax);
+  Cut cut = cut_of<KB>(a, threadIdx.x, blockIdx.x == 0);  // (warp 0 keeps its 32)
+  line_sums<KB, NTHREADS>(a, cut, warp_sums);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -381,22 +222,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLess));
   if (warp == 0) {
     // ============================================================ pieces, Q
-    int64_t line = 0, in_waves = 0, keys = 0, parts = 0;
-    for (int i = 0; i < NTHREADS / 32 && i * 32 < a.pd.N; ++i) {
-      line += sums[i * 4];
-      in_waves += sums[i * 4 + 1];
-      keys += sums[i * 4 + 2];
-      parts += sums[i * 4 + 3];
-    }
-    const bool waves = keys * a.pd.Hkv * (4 * D) > kWaveBytes;
-    const bool small = parts <= (int64_t)grid && !waves;
-    const int64_t total = small ? parts * kSlotLen : line - (waves ? in_waves : 0);
-    int64_t share = (total + grid - 1) / grid;
-    if (share < kLeastShare) share = kLeastShare;
-    if (small) {
-      share = kSlotLen;
-      if (cut.items > 0) cut_small(cut);
-    }
+    const LineSums sums = add_sums<NTHREADS>(a, warp_sums);
     int pub = 0, nq = 0;     // pieces published, their Q looked after
     int qs = 0;              // query slot of the next single tile
     uint32_t qph = 3u;       // phases of q_empty to wait for, bit = slot
@@ -475,108 +301,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       return true;
     };
 
-    bool ok = true;
-    int held = 0;  // the 32 requests this warp's lanes hold
-    auto hold = [&](int s0) {
-      if (held != s0) {
-        cut = cut_of(a, s0 + lane, false);
-        if (small && cut.items > 0) cut_small(cut);
-      }
-      held = s0;
-    };
-    // items that go in waves, all KV groups of a request together
-    auto wave_items = [&](const Cut& c) -> unsigned {
-      if (!waves || c.items <= 1 || a.pd.window != 0) return 0u;
-      const unsigned all = (unsigned)c.items * (unsigned)a.pd.Hkv;
-      return all - all % grid;
-    };
-    if (waves) {
-      for (int s0 = 0; ok && s0 < a.pd.N; s0 += 32) {
-        hold(s0);
-        const unsigned in = wave_items(cut);
-        for (unsigned m = __ballot_sync(FULL, in > 0); ok && m; m &= m - 1) {
-          const int l = __ffs(m) - 1;
-          const int q0 = __shfl_sync(FULL, cut.q0, l), ql = __shfl_sync(FULL, cut.ql, l);
-          const int kv = __shfl_sync(FULL, cut.kv, l), ipt = __shfl_sync(FULL, cut.ipt, l);
-          const unsigned items = __shfl_sync(FULL, (unsigned)cut.items, l);
-          const unsigned lim = __shfl_sync(FULL, in, l);
-          for (unsigned f = blockIdx.x; ok && f < lim; f += grid)
-            ok = publish(item_piece(a, s0 + l, q0, ql, kv, ipt, (int)(f / items), (int)(f % items)));
-        }
-      }
-    }
-    // this CTA's range of the line
-    const int64_t from = share * blockIdx.x;
-    const int64_t to = min(total, from + share);
-    int4 rec = make_int4(0, 0, 0, 0);
-    int64_t base = 0;  // the place of the 32 requests
-    for (int s0 = 0; ok && s0 < a.pd.N && base < to; s0 += 32) {
-      hold(s0);
-      const unsigned in = wave_items(cut);
-      int64_t skip = 0;  // of the request's items, those in waves
-      if (in > 0) {
-        const unsigned g = in / (unsigned)cut.items;
-        skip = cut.head * g + item_at(cut.A, cut.B, (int)(in - g * cut.items));
-      }
-      const int64_t len = cut.head * a.pd.Hkv - skip;
-      const int64_t inc = lane_scan(len);
-      for (unsigned m = __ballot_sync(FULL, len > 0 && base + inc > from && base + inc - len < to);
-           ok && m; m &= m - 1) {
-        const int l = __ffs(m) - 1;
-        const int q0 = __shfl_sync(FULL, cut.q0, l), ql = __shfl_sync(FULL, cut.ql, l);
-        const int kv = __shfl_sync(FULL, cut.kv, l), ipt = __shfl_sync(FULL, cut.ipt, l);
-        const int items = __shfl_sync(FULL, cut.items, l);
-        const unsigned tw = __shfl_sync(FULL, (unsigned)cut.tw, l);
-        const int64_t A = __shfl_sync(FULL, cut.A, l), B = __shfl_sync(FULL, cut.B, l);
-        const int64_t head = __shfl_sync(FULL, cut.head, l);
-        // the request's own coordinate of the line's place 0
-        const int64_t zero = base + __shfl_sync(FULL, inc - len - skip, l);
-        const int64_t begin = max(from, base + __shfl_sync(FULL, inc - len, l)) - zero;
-        // the group and item that hold `begin`: an estimate, put right exactly
-        int g = (int)((float)begin / (float)head);
-        g = min(max(g, 0), a.pd.Hkv - 1);
-        while (g > 0 && head * g > begin) --g;
-        while (g < a.pd.Hkv - 1 && head * (g + 1) <= begin) ++g;
-        const float y = (float)(begin - head * g), fa = (float)A - 0.5f * (float)B, fb = (float)B;
-        int k = (int)(B == 0 ? y / fa : (sqrtf(fa * fa + 2.0f * fb * y) - fa) / fb);
-        k = min(max(k, 0), items - 1);
-        while (k > 0 && head * g + item_at(A, B, k) > begin) --k;
-        while (k < items - 1 && head * g + item_at(A, B, k + 1) <= begin) ++k;
-        int64_t at = zero + head * g + item_at(A, B, k);  // the item's place
-        while (ok && at < to) {
-          Piece pc = item_piece(a, s0 + l, q0, ql, kv, ipt, g, k);
-          const int64_t cost = A + B * k;
-          // tiles whose places lie in [from, to): places at, at + tw, ...
-          const int n = pc.n;
-          auto tiles_before = [&](int64_t x) -> int {  // places before x, ends snapped
-            if (x <= at) return 0;
-            if (x - at >= cost) return n;
-            const int t = (int)min((unsigned)n, ((unsigned)(x - at) + tw - 1) / tw);
-            return share < kSnapShare || small ? t : t <= kSnap ? 0 : t >= n - kSnap ? n : t;
-          };
-          const int t0 = tiles_before(from), t1 = tiles_before(to);
-          if (n == 0 ? at >= from : t1 > t0) {
-            pc.tb += t0;
-            pc.n = t1 - t0;
-            if (pc.n < n) {
-              pc.slot = 2 * blockIdx.x + (t0 > 0 ? 0 : 1);
-              if (t0 == 0) {  // begun here, continued by the CTAs up to the last tile's
-                int c = blockIdx.x;
-                while (tiles_before(min(total, share * (c + 1))) < n) ++c;
-                rec = make_int4(pc.row0, pc.ntok, pc.g, c - (int)blockIdx.x + 1);
-              }
-            }
-            ok = publish(pc);
-          }
-          at += cost;
-          if (++k == items) {
-            k = 0;
-            if (++g == a.pd.Hkv) break;
-          }
-        }
-      }
-      base += __shfl_sync(FULL, inc, 31);
-    }
+    int4 rec;
+    bool ok = walk_line<KB>(a, cut, sums, publish, &rec);
     if (lane == 0) a.rec[blockIdx.x] = rec;  // for the merge
     if (ok) {
       Piece pc{};
@@ -1050,107 +776,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   }
 }
 
-// Merge of the cut items' partial outputs in order: lse = ln sum e^(lse_j), O =
-// sum e^(lse_j - lse) O_j.  The item that CTA c begins has its parts in slots 2 c +
-// 1, 2 c + 2, 2 c + 4, ...  All rows of all cut items are dealt out evenly, 8
-// threads to a row, so that a warp has four rows' loads in flight.
-template <int D>
-__global__ void __launch_bounds__(256) k_paged_merge(const __grid_constant__ TcArgs a) {
-  static_assert(kGrid <= 256, "a thread per CTA of the attention");
-  __shared__ int4 rec[kGrid];
-  __shared__ int ends[kGrid];  // rows of the items up to and with c
-  __shared__ int warp_sum[8];
-  const int tid = threadIdx.x, lane = tid & 31;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  int4 r = make_int4(0, 0, 0, 0);
-  if (tid < kGrid) r = a.rec[tid];
-  int inc = r.w > 1 ? r.y * a.pd.G : 0;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(FULL, inc, o);
-    if (lane >= o) inc += x;
-  }
-  if (lane == 31) warp_sum[tid >> 5] = inc;
-  __syncthreads();
-  for (int w = 0; w < tid >> 5; ++w) inc += warp_sum[w];
-  if (tid < kGrid) {
-    rec[tid] = r;
-    ends[tid] = inc;
-  }
-  __syncthreads();
-  const float ninf = -__int_as_float(0x7f800000);
-  const int l8 = lane & 7;
-  constexpr int W = D / 8;  // columns per thread
-  const unsigned octet = 0xffu << (lane & 24);
-  for (int row = blockIdx.x * 32 + (tid >> 3); row < ends[kGrid - 1]; row += gridDim.x * 32) {
-    int c = 0, hi = kGrid - 1;  // the first c with ends[c] > row
-    while (c < hi) {
-      const int mid = (c + hi) >> 1;
-      if (ends[mid] > row)
-        hi = mid;
-      else
-        c = mid + 1;
-    }
-    r = rec[c];
-    const int in = row - (ends[c] - r.y * a.pd.G);
-    const int tok = in / a.pd.G, h = in - tok * a.pd.G;
-    const int tile = tok / a.tpm;  // rows of the second query tile start at BM
-    const int64_t at = tile * BM + (tok - tile * a.tpm) * a.pd.G + h;
-    auto place = [&](int j) { return (int64_t)(2 * c + (j == 0 ? 1 : 2 * j)) * a.slot_rows + at; };
-    float mx = ninf;
-    for (int j = l8; j < r.w; j += 8) mx = fmaxf(mx, a.lpart[place(j)]);
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(octet, mx, o));
-    float acc[W], sw = 0.0f;
-#pragma unroll
-    for (int e = 0; e < W; ++e) acc[e] = 0.0f;
-#pragma unroll 2
-    for (int j = 0; j < r.w; ++j) {
-      const float lj = a.lpart[place(j)];
-      const float4* src = reinterpret_cast<const float4*>(a.opart + place(j) * D + l8 * W);
-      float4 v[W / 4];
-#pragma unroll
-      for (int e = 0; e < W / 4; ++e) v[e] = src[e];
-      const float w = lj == ninf ? 0.0f : __expf(lj - mx);
-      sw += w;
-#pragma unroll
-      for (int e = 0; e < W / 4; ++e) {  // (parts in which a row saw nothing hold zeros)
-        acc[4 * e] = fmaf(w, v[e].x, acc[4 * e]);
-        acc[4 * e + 1] = fmaf(w, v[e].y, acc[4 * e + 1]);
-        acc[4 * e + 2] = fmaf(w, v[e].z, acc[4 * e + 2]);
-        acc[4 * e + 3] = fmaf(w, v[e].w, acc[4 * e + 3]);
-      }
-    }
-    const float inv = sw > 0.0f ? 1.0f / sw : 0.0f;
-    const int64_t t = r.x + tok, hq = (int64_t)r.z * a.pd.G + h;
-    uint4* dst = reinterpret_cast<uint4*>(a.O + (t * a.pd.H + hq) * D + l8 * W);
-#pragma unroll
-    for (int e = 0; e < W / 8; ++e)
-      dst[e] = make_uint4(pack_bf16x2(acc[8 * e] * inv, acc[8 * e + 1] * inv),
-                          pack_bf16x2(acc[8 * e + 2] * inv, acc[8 * e + 3] * inv),
-                          pack_bf16x2(acc[8 * e + 4] * inv, acc[8 * e + 5] * inv),
-                          pack_bf16x2(acc[8 * e + 6] * inv, acc[8 * e + 7] * inv));
-    if (l8 == 0) a.lse[hq * a.pd.T + t] = sw > 0.0f ? mx + logf(sw) : ninf;
-  }
-}
-
-constexpr int kSlots = 2 * kGrid;  // the first and the last piece of a CTA
-
 int slot_rows(const PagedDims& pd) {
   const int64_t rows = (int64_t)pd.T * pd.G;
   return (int)(rows < BM ? rows : 2 * BM);
-}
-
-struct Ws {
-  size_t lpart, opart, bytes;
-};
-Ws carve(const PagedDims& pd) {
-  Ws w;
-  const size_t rows = (size_t)kSlots * slot_rows(pd);
-  w.lpart = ((size_t)kGrid * 16 + 255) & ~size_t(255);
-  w.opart = w.lpart + ((rows * 4 + 255) & ~size_t(255));
-  w.bytes = w.opart + rows * pd.d * 4;
-  return w;
 }
 
 // Q [T][H][d] with row stride qs, boxes of one query tile's heads and tokens.
@@ -1182,43 +810,27 @@ int launch(const TcArgs& a, const PagedAttnArgs& pa, cudaStream_t st) {
   k_paged_attn<D><<<kGrid, NTHREADS, C::SMEM, st>>>(mq, mk, mv, a);
   log_end(st);
   if (cudaGetLastError() != cudaSuccess) return SGQA_ERR_CUDA;
-  // the merge is scheduled while the attention drains and waits for its end
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * kGrid);
-  cfg.blockDim = dim3(256);
-  cfg.stream = st;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  log_begin(SGQA_K_PAGED_ATTN, st);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, k_paged_merge<D>, a);
-  log_end(st);
-  return e == cudaSuccess ? SGQA_OK : SGQA_ERR_CUDA;
+  return launch_merge<__nv_bfloat16, D, kGrid, 256>(a, a.O, a.lse, st);
 }
 
 }  // namespace
 
 size_t paged_tc_ws_bytes(const PagedDims& pd) {
-  return pd.N == 0 || pd.T == 0 ? 0 : carve(pd).bytes;
+  return pd.N == 0 || pd.T == 0 ? 0 : carve_line(kGrid, slot_rows(pd), pd.d).bytes;
 }
 
 int launch_paged_tc(const PagedDims& pd, const PagedAttnArgs& pa, void* ws, cudaStream_t st) {
-  const Ws w = carve(pd);
-  uint8_t* base = static_cast<uint8_t*>(ws);
   TcArgs a;
-  a.pd = pd;
-  a.page_table = pa.page_table;
-  a.q_start = pa.q_start;
-  a.kv_len = pa.kv_len;
+  a.slot_rows = slot_rows(pd);
+  set_line(a, pd, pa, carve_line(kGrid, a.slot_rows, pd.d), ws);
+  a.groups = pd.Hkv;
+  a.head_parts = 1;
+  a.heads = pd.G;
+  a.tpm = BM / pd.G;
+  a.tiles_per_item = 2;
+  a.tile_rows = BM;
   a.O = static_cast<__nv_bfloat16*>(pa.O);
   a.lse = pa.lse;
-  a.rec = reinterpret_cast<int4*>(base);
-  a.lpart = reinterpret_cast<float*>(base + w.lpart);
-  a.opart = reinterpret_cast<float*>(base + w.opart);
-  a.status = pa.status;
-  a.slot_rows = slot_rows(pd);
   int x = pd.ps, y = KB;
   while (y) {
     const int t = x % y;
@@ -1226,11 +838,8 @@ int launch_paged_tc(const PagedDims& pd, const PagedAttnArgs& pa, void* ws, cuda
     y = t;
   }
   a.box = x;
-  a.tpm = BM / pd.G;
   a.wide = (reinterpret_cast<uintptr_t>(pa.O) & 31u) == 0;
   a.sl2 = pd.scale * 1.4426950408889634f;
-  // windows and lengths end at cap: the sums of both stay in 32 bits
-  if (a.pd.window > pd.cap) a.pd.window = pd.cap;
   // whole items of a request, over its KV groups, are counted in 32 bits
   if ((int64_t)pd.Hkv * ((int64_t)pd.T / a.tpm + 1) > 0x7fffffffll) return SGQA_ERR_UNSUPPORTED;
   return pd.d == 128 ? launch<128>(a, pa, st) : launch<64>(a, pa, st);
