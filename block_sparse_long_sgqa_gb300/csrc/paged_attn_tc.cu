@@ -829,6 +829,10 @@ int launch_paged_tc(const PagedDims& pd, const PagedAttnArgs& pa, void* ws, cuda
   a.tpm = BM / pd.G;
   a.tiles_per_item = 2;
   a.tile_rows = BM;
+  // 0.6 us a tile: four short contexts 16.8 us, one of 8K keys 23.2 (12 and 4: 17.2
+  // and 25.5; 8 and 8: 18.0 and 23.4; cut evenly over all CTAs: 20.0 and 27.4)
+  a.whole = 8;
+  a.part = 6;
   a.O = static_cast<__nv_bfloat16*>(pa.O);
   a.lse = pa.lse;
   int x = pd.ps, y = KB;

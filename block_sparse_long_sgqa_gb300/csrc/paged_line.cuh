@@ -31,6 +31,7 @@ struct LineArgs {
   int heads;             // query heads of a group (the last of a KV head: at most)
   int tpm;               // tokens of a query tile
   int tiles_per_item;    // query tiles of an item of longer requests: 1 or 2
+  int whole, part;       // key tiles of an uncut item and of a part, in small calls
   int tile_rows;         // rows from one query tile of a partial output to the next
   int slot_rows;
   float *opart, *lpart;  // partial outputs [slot][slot_rows][D], their lse [slot][slot_rows];
@@ -57,11 +58,10 @@ constexpr int kWtSingle = 2, kWtDouble = 3;
 constexpr int kOver = 3;
 // Shortest range of a CTA, in key tiles of a single query tile.
 constexpr int kLeastTiles = 2;
-// Small calls: items of up to kWhole key tiles are not cut at all, longer ones into
-// parts of kPart tiles, when that makes no more pieces than there are CTAs.  Each
-// piece is then one CTA's range, kSlotLen long.  (A cut costs its merge, about
-// 4 us; a CTA takes 0.6 us a tile.)
-constexpr int kWhole = 8, kPart = 6;
+// Small calls: items of up to `whole` key tiles are not cut at all, longer ones into
+// parts of `part` tiles, when that makes no more pieces than there are CTAs.  Each
+// piece is then one CTA's range, kSlotLen long.  A cut costs its merge, about 4 us;
+// what a tile takes decides (LineArgs).
 constexpr int64_t kSlotLen = int64_t(1) << 20;
 // A range that ends within kSnap tiles of an item's beginning or end leaves the
 // item whole, when ranges are long enough for that to leave no part empty.
@@ -80,11 +80,11 @@ struct Cut {
   int64_t A, B, head;   // head: all items of a KV group
 };
 // Pieces of each of the request's items in a small call.
-__device__ __forceinline__ int parts_of(const Cut& c) {
-  return c.tiles <= kWhole ? 1 : (int)((unsigned)(c.tiles + kPart - 1) / (unsigned)kPart);
+__device__ __forceinline__ int parts_of(const LineArgs& a, const Cut& c) {
+  return c.tiles <= a.whole ? 1 : (int)((unsigned)(c.tiles + a.part - 1) / (unsigned)a.part);
 }
-__device__ __forceinline__ void cut_small(Cut& c) {
-  const int parts = parts_of(c);
+__device__ __forceinline__ void cut_small(const LineArgs& a, Cut& c) {
+  const int parts = parts_of(a, c);
   c.A = parts * kSlotLen;
   c.B = 0;
   c.head = c.A * c.items;
@@ -186,7 +186,7 @@ __device__ __forceinline__ void line_sums(const LineArgs& a, const Cut& cut, int
   for (int s = threadIdx.x; s < a.pd.N; s += NT) {
     const Cut c = s < NT ? cut : cut_of<KB>(a, s, blockIdx.x == 0);
     line += c.head * a.groups;
-    parts += (int64_t)parts_of(c) * c.items * a.groups;
+    parts += (int64_t)parts_of(a, c) * c.items * a.groups;
     if (c.items > 1 && a.pd.window == 0) {
       const unsigned all = (unsigned)c.items * (unsigned)a.groups, in = all - all % grid;
       const unsigned g = in / (unsigned)c.items;
@@ -237,14 +237,14 @@ __device__ __forceinline__ bool walk_line(const LineArgs& a, Cut cut, const Line
   if (share < kLeastTiles * KB * kWtSingle) share = kLeastTiles * KB * kWtSingle;
   if (small) {
     share = kSlotLen;
-    if (cut.items > 0) cut_small(cut);
+    if (cut.items > 0) cut_small(a, cut);
   }
   bool ok = true;
   int held = 0;  // the 32 requests this warp's lanes hold
   auto hold = [&](int s0) {
     if (held != s0) {
       cut = cut_of<KB>(a, s0 + lane, false);
-      if (small && cut.items > 0) cut_small(cut);
+      if (small && cut.items > 0) cut_small(a, cut);
     }
     held = s0;
   };
