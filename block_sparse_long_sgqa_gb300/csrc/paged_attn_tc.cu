@@ -501,22 +501,48 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           }
         }
       } else {
-        auto qk_when = [&](int j) -> bool {
-          if ((j & sh) == 0 && !warp_poll(&k_full[ks], kph, ab, a.status, 337)) return false;
-          qk(j);
-          return true;
+        // The product with P, and behind it the next S, which overwrites P: products
+        // of one thread run in issue order.  The next key tile is looked for while P
+        // is waited for, so that the two are issued without a pause.
+        auto k_there = [&](int j) -> bool {
+          return (j & sh) != 0 || warp_poll(&k_full[ks], kph, ab, a.status, 337);
         };
-        ok = J == 0 || (qk_when(0) && (J < 2 || qk_when(1)));
+        for (int j = 0; ok && j < 2 && j < J; ++j) {
+          ok = k_there(j);
+          if (ok) qk(j);
+        }
         for (int j = 0; ok && j < J; ++j) {
           const int g = j & 1;
-          ok = ((j & sh) != 0 || warp_poll(&v_full[vs], vph, ab, a.status, 338)) &&
-               warp_poll(&p_full[g], (pph >> g) & 1u, ab, a.status, 339);
+          const bool next = j + 2 < J;
+          bool key = !next || (j & sh) != 0;
+          uint64_t t_prog = 0;
+          for (uint32_t i2 = 0;; ++i2) {
+            const bool there = mbar_test(&p_full[g], (pph >> g) & 1u) &
+                               ((j & sh) != 0 || mbar_test(&v_full[vs], vph));
+            if (!key) key = __all_sync(FULL, mbar_test(&k_full[ks], kph));
+            if (__all_sync(FULL, there)) break;
+            if ((i2 & 255) == 255) {
+              if (t_prog == 0) t_prog = globaltimer();
+              int stop = 0;
+              if (ab.set()) {
+                stop = 1;
+              } else if (globaltimer() - t_prog > kWaitLimitNs) {
+                if (lane == 0) ab.raise(a.status, 339);
+                stop = 1;
+              }
+              if (__any_sync(FULL, stop)) {
+                ok = false;
+                break;
+              }
+            }
+          }
           if (!ok) break;
           pph ^= 1u << g;
           pv(j);
-          // products of one thread run in issue order, so this S overwrites P
-          // only after the product above has read it
-          if (j + 2 < J) ok = qk_when(j + 2);
+          if (next) {
+            if (!key) ok = k_there(j + 2);
+            if (ok) qk(j + 2);
+          }
         }
       }
       if (single && n > 0) qs ^= 1;
