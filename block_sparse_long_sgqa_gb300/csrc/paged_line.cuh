@@ -297,13 +297,17 @@ __device__ __forceinline__ bool walk_line(const LineArgs& a, Cut cut, const Line
       const int64_t zero = base + __shfl_sync(FULL, inc - len - skip, l);
       const int64_t begin = max(from, base + __shfl_sync(FULL, inc - len, l)) - zero;
       // the group and item that hold `begin`: an estimate, put right exactly
-      int g = (int)((float)begin / (float)head);
-      g = min(max(g, 0), a.groups - 1);
+      int g = 0, k = 0;
+      if (head <= begin) g = min((int)__fdividef((float)begin, (float)head), a.groups - 1);
       while (g > 0 && head * g > begin) --g;
       while (g < a.groups - 1 && head * (g + 1) <= begin) ++g;
-      const float y = (float)(begin - head * g), fa = (float)A - 0.5f * (float)B, fb = (float)B;
-      int k = (int)(B == 0 ? y / fa : (sqrtf(fa * fa + 2.0f * fb * y) - fa) / fb);
-      k = min(max(k, 0), items - 1);
+      const int64_t in_group = begin - head * g;
+      if (items > 1 && in_group >= A) {
+        const float y = (float)in_group, fa = (float)A - 0.5f * (float)B, fb = (float)B;
+        k = (int)(B == 0 ? __fdividef(y, fa)
+                         : __fdividef(__fsqrt_rn(fa * fa + 2.0f * fb * y) - fa, fb));
+        k = min(max(k, 0), items - 1);
+      }
       while (k > 0 && head * g + item_at(A, B, k) > begin) --k;
       while (k < items - 1 && head * g + item_at(A, B, k + 1) <= begin) ++k;
       int64_t at = zero + head * g + item_at(A, B, k);  // the item's place
