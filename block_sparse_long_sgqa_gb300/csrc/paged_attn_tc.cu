@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   if (warp != 0) asm volatile("bar.sync 1, 384;" ::: "memory");
   // Registers: a softmax thread holds a row's 128 scores.  2 x 128 x kRegsMore +
   // 128 x kRegsLess stays within the 384 x 168 of the launch.
-  constexpr int kRegsLess = 80, kRegsMore = 208;
+  constexpr int kRegsLess = 88, kRegsMore = 208;
   static_assert(256 * kRegsMore + 128 * kRegsLess <= NTHREADS * 168, "the launch's registers");
   if (warp < 4) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLess));

@@ -383,6 +383,11 @@ ATTN = {
     "scale": ([9, 1], [100, 222], 8, 2, 64, 16, dict(softmax_scale=0.5)),
     "padding": ([3, 1], [40, 200], 8, 2, 128, 16, dict(pad=70)),
     "fused_rows": ([20, 1], [150, 33], 8, 2, 64, 16, dict(fused=True)),
+    # one request over every CTA, and more requests than threads look at first
+    "decode_split": ([1], [30000], 1, 1, 128, 64, {}),
+    "decode_split_16": ([1], [20011], 16, 1, 64, 32, {}),
+    "many_requests": ([1, 0, 1] * 150, [(7 * i) % 131 + 1 for i in range(450)], 4, 2, 64, 16, {}),
+    "many_chunks": ([1, 40, 0, 17] * 20, [60 + 31 * (i % 9) for i in range(80)], 8, 2, 64, 16, {}),
     "one_head_many_tiles": ([1000], [1300], 4, 1, 64, 32, {}),
 }
 
@@ -529,6 +534,170 @@ def test_attention_other_stream(s):
     s.sgqa_paged_attn(p, Q, Kd, Vd, pt, qs, kv, O, lse, ws, stream=st)
     st.synchronize()
     check_attn(s, b, p, wide, K, V, q_start, kw, O, lse)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_attention_waves(s, dtype):
+    """Two requests whose shared keys exceed what L2 holds: whole items go out in
+    waves first, the rest of each request evenly; checked on spread rows."""
+    d, hk, ps = 128, 8, 64
+    H = 64 if dtype == "bf16" else 16
+    b = Batch(8, [700, 650], [20011, 15000], ps, held_at="after")
+    T = 1350
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    p = params(s, n_seqs=2, max_tokens=T, n_q_heads=H, n_kv_heads=hk, head_dim=d, page_size=ps,
+               n_pages=b.n_pages, max_pages=b.max_pages,
+               dtype=s.BF16 if dtype == "bf16" else s.FP32)
+    torch.manual_seed(3)
+    Q = torch.randn(T, H, d, device="cuda").to(dt)
+    K, V = (torch.randn(b.n_pages, hk, ps, d, device="cuda").to(dt) for _ in "KV")
+    q_start = np.array([0, 700, 1350], np.int32)
+    O, lse, code = run_attn(s, p, Q.cpu(), K, V, b.table, q_start, b.kv)
+    assert code == s.OK
+    O, lse = O.double().cpu().numpy(), lse.double().cpu().numpy()
+    assert np.isfinite(O).all() and np.isfinite(lse).all()
+    Kn, Vn, Qn = (x.double().cpu().numpy() for x in (K, V, Q))
+    for r in range(2):
+        for i in (0, 1, 31, 32, 333, int(b.q[r]) - 1):  # one row as a batch of its own
+            t = int(q_start[r]) + i
+            n = int(b.kv[r] - b.q[r]) + i + 1
+            R, z, tO, tl, _ = ref.attention(Qn[t:t + 1], Kn, Vn, ps, b.table[r:r + 1],
+                                            [0, 1], [n], ref.default_scale(d), True, 0,
+                                            dtype == "bf16")
+            assert (np.abs(O[t] - R[0]) <= tO[0]).all(), (r, i)
+            assert (np.abs(lse[:, t] - z[:, 0]) <= tl[:, 0]).all(), (r, i)
+
+
+@gpu
+def test_offsets_past_4_gib(s):
+    """Pages at the far end of a pool of more than 4 GiB: rows appended there are
+    found by the attention, and nothing else of the pool is touched."""
+    d, hk, H, ps, n_pages = 128, 8, 16, 64, 40000   # 5.2 GB for K, as much for V
+    p = params(s, n_seqs=1, max_tokens=150, n_q_heads=H, n_kv_heads=hk, head_dim=d, page_size=ps,
+               n_pages=n_pages, max_pages=3)
+    Kp, Vp = (torch.zeros(n_pages, hk, ps, d, dtype=torch.bfloat16, device="cuda") for _ in "KV")
+    torch.manual_seed(4)
+    Q = torch.randn(150, H, d, device="cuda").bfloat16()
+    K, V = (torch.randn(150, hk, d, device="cuda").bfloat16() for _ in "KV")
+    table = np.array([[n_pages - 1, 2, n_pages - 2]], np.int32)
+    pos = np.arange(150)
+    slots = table[0, pos // ps].astype(np.int64) * ps + pos % ps
+    st = s.new_status()
+    s.sgqa_paged_append(p, K, V, dev(slots), Kp, Vp, status=st)
+    O, lse = torch.zeros_like(Q), torch.zeros(H, 150, device="cuda")
+    s.sgqa_paged_attn(p, Q, Kp, Vp, dev(table), dev(np.array([0, 150], np.int32)),
+                      dev(np.array([150], np.int32)), O, lse, s.alloc_paged_workspace(p), status=st)
+    assert status_of(s, st) == s.OK
+    assert torch.equal(Kp[n_pages - 1].transpose(0, 1), K[:64])
+    used = Kp.view(torch.int16).ne(0).flatten(1).any(1).nonzero().flatten().tolist()
+    assert used == [2, n_pages - 2, n_pages - 1]
+    Kl, Vl = (x.double().cpu().numpy().transpose(1, 0, 2)[None] for x in (K, V))
+    R, z, tO, tl, _ = ref.attention(Q.double().cpu().numpy(), Kl, Vl, 150, np.zeros((1, 1), int),
+                                    [0, 150], [150], ref.default_scale(d), True, 0, True)
+    assert (np.abs(O.double().cpu().numpy() - R) <= tO).all()
+    assert (np.abs(lse.double().cpu().numpy() - z) <= tl).all()
+
+
+@gpu
+def test_attention_output_at_16_bytes(s):
+    """O and Q that are 16-byte but not 32-byte aligned, rows before and behind kept."""
+    b, p, wide, K, V, q_start, kw = attn_case(s, "chunk", "bf16")
+    n = p.max_tokens * p.n_q_heads * p.head_dim
+    raw = torch.full((n + 24,), 5.0, dtype=torch.bfloat16, device="cuda")
+    O = raw[8:8 + n].view(p.max_tokens, p.n_q_heads, p.head_dim)
+    q_raw = torch.zeros(n + 8, dtype=torch.bfloat16, device="cuda")
+    q_raw[8:] = wide.cuda().flatten()
+    Q = q_raw[8:].view_as(O)
+    assert O.data_ptr() % 32 == 16 and Q.data_ptr() % 32 == 16
+    lse = torch.full((p.n_q_heads, p.max_tokens), 7.0).cuda()
+    s.sgqa_paged_attn(p, Q, K.cuda(), V.cuda(), dev(b.table), dev(q_start), dev(b.kv), O, lse,
+                      s.alloc_paged_workspace(p))
+    check_attn(s, b, p, wide, K, V, q_start, kw, O, lse)
+    assert (raw[:8] == 5.0).all() and (raw[8 + n:] == 5.0).all()
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_attention_graphs_share_a_workspace(s, dtype):
+    """Two captured calls of different shapes over one workspace, replayed in turn
+    and with other lengths, give what the same calls give eagerly on their own."""
+    cases, graphs = [], []
+    parts = [attn_case(s, name, dtype) for name in ("decode_long", "mixed_idle")]
+    ws = torch.empty(max(s.paged_workspace_bytes(c[1]) for c in parts), dtype=torch.uint8,
+                     device="cuda")
+    for b, p, wide, K, V, q_start, kw in parts:
+        t = dict(Q=wide.cuda(), K_pages=K.cuda(), V_pages=V.cuda(), page_table=dev(b.table),
+                 q_start=dev(q_start), kv_len=dev(b.kv))
+        O = torch.full(wide.shape, 3.0, dtype=wide.dtype, device="cuda")
+        lse = torch.full((p.n_q_heads, p.max_tokens), 7.0, device="cuda")
+        s.sgqa_paged_attn(p, **t, O=O, lse=lse, ws=ws)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            s.sgqa_paged_attn(p, **t, O=O, lse=lse, ws=ws)
+        cases.append((b, p, t, O, lse))
+        graphs.append(g)
+    for it in range(3):
+        for g, (b, p, t, O, lse) in zip(graphs, cases):
+            t["kv_len"].copy_(dev(np.maximum(b.kv - 3 * it, 0)))
+            g.replay()
+        for b, p, t, O, lse in cases:
+            O2, l2 = torch.full_like(O, 3.0), torch.full_like(lse, 7.0)
+            s.sgqa_paged_attn(p, **t, O=O2, lse=l2, ws=s.alloc_paged_workspace(p))
+            assert torch.equal(O, O2) and torch.equal(lse, l2), it
+
+
+@gpu
+def test_attention_calls_at_once(s):
+    """Calls on two streams with a workspace each."""
+    outs = []
+    work = [attn_case(s, name, "bf16") for name in ("chunk", "decode_long")]
+    args = []
+    for b, p, wide, K, V, q_start, kw in work:
+        args.append(dict(Q=wide.cuda(), K_pages=K.cuda(), V_pages=V.cuda(),
+                         page_table=dev(b.table), q_start=dev(q_start), kv_len=dev(b.kv),
+                         O=torch.full(wide.shape, 3.0, dtype=wide.dtype, device="cuda"),
+                         lse=torch.full((p.n_q_heads, p.max_tokens), 7.0, device="cuda"),
+                         ws=s.alloc_paged_workspace(p)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in work]
+    for _ in range(20):
+        for w, a, st in zip(work, args, streams):
+            s.sgqa_paged_attn(w[1], **a, stream=st)
+    torch.cuda.synchronize()
+    for (b, p, wide, K, V, q_start, kw), a in zip(work, args):
+        check_attn(s, b, p, wide, K, V, q_start, kw, a["O"], a["lse"])
+
+
+@gpu
+def test_stalled_wait_reports_timeout_and_recovers(s):
+    """The debug request of the status word makes the first piece's pipeline give up
+    after 1 ms: the status says so, and the next call on the same buffers is right."""
+    b, p, wide, K, V, q_start, kw = attn_case(s, "chunk", "bf16")
+    a = dict(Q=wide.cuda(), K_pages=K.cuda(), V_pages=V.cuda(), page_table=dev(b.table),
+             q_start=dev(q_start), kv_len=dev(b.kv),
+             O=torch.full(wide.shape, 3.0, dtype=wide.dtype, device="cuda"),
+             lse=torch.full((p.n_q_heads, p.max_tokens), 7.0, device="cuda"),
+             ws=s.alloc_paged_workspace(p))
+    st = s.new_status()
+    st[3] = s.DEBUG_STALL
+    s.sgqa_paged_attn(p, **a, status=st)
+    code, detail = s.read_status(st)
+    assert code == s.ERR_TIMEOUT and detail == 220, (s.status_string(code), detail)
+    s.reset_status(st)
+    s.sgqa_paged_attn(p, **a, status=st)
+    assert status_of(s, st) == s.OK
+    check_attn(s, b, p, wide, K, V, q_start, kw, a["O"], a["lse"])
+
+
+@gpu
+def test_launch_log_names_the_kernels(s):
+    b, p, wide, K, V, q_start, kw = attn_case(s, "chunk", "bf16")
+    with s.launch_log(8) as log:
+        run_attn(s, p, wide, K, V, b.table, q_start, b.kv)
+    torch.cuda.synchronize()
+    assert [k for k, _ in log.entries()] == [s.K_PAGED_ATTN] * 2  # the attention and its merge
 
 
 # ------------------------------------------------------- the operators together
