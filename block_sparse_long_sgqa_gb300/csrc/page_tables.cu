@@ -138,6 +138,8 @@ __global__ void __launch_bounds__(NT)
                 int64_t* __restrict__ slot_map, int32_t* __restrict__ positions,
                 int32_t* n_free_out, int32_t* status) {
   __shared__ Shared sh;
+  pdl_next();
+  pdl_wait();
   const int ntile = (pd.N + TILE - 1) / TILE;
   const int n_free = *n_free_p;
   if (threadIdx.x == 0) sh.bad = 0;
@@ -235,6 +237,8 @@ __global__ void __launch_bounds__(NT)
                    int32_t* free_pages, const int32_t* __restrict__ n_free_p,
                    int32_t* n_free_out, int32_t* status) {
   __shared__ Shared sh;
+  pdl_next();
+  pdl_wait();
   const int ntile = (pd.N + TILE - 1) / TILE;
   const int n_free = *n_free_p;
   if (threadIdx.x == 0) sh.bad = 0;
@@ -310,10 +314,10 @@ int launch_page_plan(const PagedDims& pd, const int32_t* q_len, const int32_t* k
   const int64_t want = ((int64_t)pd.T + NT - 1) / NT;
   const unsigned grid = (unsigned)(want < 1 ? 1 : want < kSMs ? want : kSMs);
   log_begin(SGQA_K_PAGES, st);
-  k_page_plan<<<grid, NT, 0, st>>>(pd, q_len, kv_len, free_pages, n_free, page_table, q_start,
-                                   slot_map, positions, n_free_out, status);
+  const cudaError_t e = launch_pdl(k_page_plan, grid, NT, 0, st, pd, q_len, kv_len, free_pages, n_free,
+                                   page_table, q_start, slot_map, positions, n_free_out, status);
   log_end(st);
-  return cudaGetLastError() == cudaSuccess ? SGQA_OK : SGQA_ERR_CUDA;
+  return e == cudaSuccess ? SGQA_OK : SGQA_ERR_CUDA;
 }
 
 int launch_page_release(const PagedDims& pd, const int32_t* kv_len, const int32_t* keep_len,
@@ -323,10 +327,10 @@ int launch_page_release(const PagedDims& pd, const int32_t* kv_len, const int32_
   const int64_t want = (most + NT - 1) / NT;
   const unsigned grid = (unsigned)(want < 1 ? 1 : want < kSMs ? want : kSMs);
   log_begin(SGQA_K_PAGES, st);
-  k_page_release<<<grid, NT, 0, st>>>(pd, kv_len, keep_len, page_table, free_pages, n_free,
-                                      n_free_out, status);
+  const cudaError_t e = launch_pdl(k_page_release, grid, NT, 0, st, pd, kv_len, keep_len, page_table,
+                                   free_pages, n_free, n_free_out, status);
   log_end(st);
-  return cudaGetLastError() == cudaSuccess ? SGQA_OK : SGQA_ERR_CUDA;
+  return e == cudaSuccess ? SGQA_OK : SGQA_ERR_CUDA;
 }
 
 }  // namespace sgqa

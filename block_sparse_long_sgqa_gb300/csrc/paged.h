@@ -48,6 +48,31 @@ int launch_paged_simt(const PagedDims& pd, const PagedAttnArgs& a, void* ws, cud
 size_t paged_tc_ws_bytes(const PagedDims& pd);
 int launch_paged_tc(const PagedDims& pd, const PagedAttnArgs& a, void* ws, cudaStream_t st);
 
+// Launches in a row: each kernel lets the next one be scheduled from its start on
+// (pdl_next) and, before it touches memory that another kernel may still read or write,
+// waits until the one before it is complete (pdl_wait).  The next launch's latency and
+// set-up then lie beside the end of this one's work.
+__device__ __forceinline__ void pdl_next() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... P, typename... A>
+inline cudaError_t launch_pdl(void (*kernel)(P...), int64_t grid, int threads, size_t smem,
+                              cudaStream_t st, const A&... args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Lengths of request s as the kernels use them: rows [q0, q0 + ql) and kv
 // cached positions; ql = 0 and a report where they do not fit the call.
 struct SeqLen {

@@ -10,6 +10,8 @@ __global__ void __launch_bounds__(256)
     k_paged_append(PagedDims pd, const uint4* __restrict__ K, const uint4* __restrict__ V,
                    const int64_t* __restrict__ slot_map, uint4* __restrict__ Kp,
                    uint4* __restrict__ Vp, int log_up, int64_t row_units, int32_t* status) {
+  pdl_next();
+  pdl_wait();
   const int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (t >= pd.T) return;
   const int lane = threadIdx.x & 31;
@@ -41,11 +43,12 @@ int launch_paged_append(const PagedDims& pd, const void* K, const void* V,
   const int up = pd.d * pd.elem / 16;  // 8, 16 or 32
   const int log_up = up == 8 ? 3 : up == 16 ? 4 : 5;
   log_begin(SGQA_K_APPEND, st);
-  k_paged_append<<<(unsigned)((pd.T + 7) / 8), 256, 0, st>>>(
-      pd, static_cast<const uint4*>(K), static_cast<const uint4*>(V), slot_map,
-      static_cast<uint4*>(Kp), static_cast<uint4*>(Vp), log_up, pd.kvs * pd.elem / 16, status);
+  const cudaError_t e = launch_pdl(
+      k_paged_append, ((int64_t)pd.T + 7) / 8, 256, 0, st, pd, static_cast<const uint4*>(K),
+      static_cast<const uint4*>(V), slot_map, static_cast<uint4*>(Kp), static_cast<uint4*>(Vp),
+      log_up, pd.kvs * pd.elem / 16, status);
   log_end(st);
-  return cudaGetLastError() == cudaSuccess ? SGQA_OK : SGQA_ERR_CUDA;
+  return e == cudaSuccess ? SGQA_OK : SGQA_ERR_CUDA;
 }
 
 }  // namespace sgqa

@@ -243,7 +243,8 @@ __global__ void __launch_bounds__(NT, (Cfg<D, RPT>::PER_SM))
     k_paged_simt(const __grid_constant__ SimtArgs a) {
   extern __shared__ __align__(16) float sm[];
   __shared__ int64_t warp_sums[NT / 32][4];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  pdl_next();
+  pdl_wait();
   {
     const Cut mine = cut_of<KT>(a, threadIdx.x, blockIdx.x == 0);
     line_sums<KT, NT>(a, mine, warp_sums);
@@ -274,9 +275,9 @@ int launch(const SimtArgs& a, cudaStream_t st) {
                            C::SMEM) != cudaSuccess)
     return SGQA_ERR_CUDA;
   log_begin(SGQA_K_PAGED_ATTN, st);
-  k_paged_simt<D, RPT><<<C::GRID, NT, C::SMEM, st>>>(a);
+  const cudaError_t e = launch_pdl(k_paged_simt<D, RPT>, C::GRID, NT, C::SMEM, st, a);
   log_end(st);
-  if (cudaGetLastError() != cudaSuccess) return SGQA_ERR_CUDA;
+  if (e != cudaSuccess) return SGQA_ERR_CUDA;
   return launch_merge<float, D, C::GRID, (C::GRID + 31) / 32 * 32>(a, a.O, a.lse, st);
 }
 
@@ -299,6 +300,7 @@ int launch_paged_simt(const PagedDims& pd, const PagedAttnArgs& pa, void* ws, cu
   a.tile_rows = 0;
   a.whole = 2;  // 3 us a tile
   a.part = 1;
+  a.uncut = pd.cap <= a.whole * KT;
   a.Q = static_cast<const float*>(pa.Q);
   a.K = static_cast<const float*>(pa.K);
   a.V = static_cast<const float*>(pa.V);

@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                  const __grid_constant__ CUtensorMap mv, const __grid_constant__ TcArgs a) {
   using C = Cfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  pdl_next();
   if (smem_u32(smem) & 1023u) {  // the operand tiles' swizzle needs it
     if (blockIdx.x == 0 && threadIdx.x == 0) report(a.status, SGQA_ERR_BOUNDS, 330);
     return;
@@ -199,6 +199,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     fence_mbar_init();
   }
   if (warp == 3) tmem_alloc(tmem_slot, 512);
+  pdl_wait();
   if (lane == 0 && warp >= 1 && warp <= 3) tma_prefetch_desc(warp == 1 ? &mk : warp == 2 ? &mv : &mq);
 
   // ---- the line: its length, the part of it that waves would take, and the keys
@@ -833,9 +834,9 @@ int launch(const TcArgs& a, const PagedAttnArgs& pa, cudaStream_t st) {
       cudaSuccess)
     return SGQA_ERR_CUDA;
   log_begin(SGQA_K_PAGED_ATTN, st);
-  k_paged_attn<D><<<kGrid, NTHREADS, C::SMEM, st>>>(mq, mk, mv, a);
+  const cudaError_t e = launch_pdl(k_paged_attn<D>, kGrid, NTHREADS, C::SMEM, st, mq, mk, mv, a);
   log_end(st);
-  if (cudaGetLastError() != cudaSuccess) return SGQA_ERR_CUDA;
+  if (e != cudaSuccess) return SGQA_ERR_CUDA;
   return launch_merge<__nv_bfloat16, D, kGrid, 256>(a, a.O, a.lse, st);
 }
 
@@ -859,6 +860,7 @@ int launch_paged_tc(const PagedDims& pd, const PagedAttnArgs& pa, void* ws, cuda
   // and 25.5; 8 and 8: 18.0 and 23.4; cut evenly over all CTAs: 20.0 and 27.4)
   a.whole = 8;
   a.part = 6;
+  a.uncut = pd.cap <= a.whole * KB;
   a.O = static_cast<__nv_bfloat16*>(pa.O);
   a.lse = pa.lse;
   int x = pd.ps, y = KB;

@@ -32,6 +32,7 @@ struct LineArgs {
   int tpm;               // tokens of a query tile
   int tiles_per_item;    // query tiles of an item of longer requests: 1 or 2
   int whole, part;       // key tiles of an uncut item and of a part, in small calls
+  int uncut;             // no item is longer than `whole`: none is ever cut, nothing to merge
   int tile_rows;         // rows from one query tile of a partial output to the next
   int slot_rows;
   float *opart, *lpart;  // partial outputs [slot][slot_rows][D], their lse [slot][slot_rows];
@@ -58,11 +59,6 @@ constexpr int kWtSingle = 2, kWtDouble = 3;
 constexpr int kOver = 3;
 // Shortest range of a CTA, in key tiles of a single query tile.
 constexpr int kLeastTiles = 2;
-// Small calls: items of up to `whole` key tiles are not cut at all, longer ones into
-// parts of `part` tiles, when that makes no more pieces than there are CTAs.  Each
-// piece is then one CTA's range, kSlotLen long.  A cut costs its merge, about 4 us;
-// what a tile takes decides (LineArgs).
-constexpr int64_t kSlotLen = int64_t(1) << 20;
 // A range that ends within kSnap tiles of an item's beginning or end leaves the
 // item whole, when ranges are long enough for that to leave no part empty.
 constexpr int kSnap = 2;
@@ -79,16 +75,9 @@ struct Cut {
   int tiles;            // most key tiles of an item
   int64_t A, B, head;   // head: all items of a KV group
 };
-// Pieces of each of the request's items in a small call.
+// Parts of each of the request's items in a small call (see walk_line).
 __device__ __forceinline__ int parts_of(const LineArgs& a, const Cut& c) {
   return c.tiles <= a.whole ? 1 : (int)((unsigned)(c.tiles + a.part - 1) / (unsigned)a.part);
-}
-__device__ __forceinline__ void cut_small(const LineArgs& a, Cut& c) {
-  const int parts = parts_of(a, c);
-  c.A = parts * kSlotLen;
-  c.B = 0;
-  c.head = c.A * c.items;
-  c.tw = c.tiles > 1 ? (int)((unsigned)c.A / (unsigned)c.tiles) : (int)kSlotLen;
 }
 template <int KB>
 __device__ __forceinline__ Cut cut_of(const LineArgs& a, int s, bool tell) {
@@ -230,22 +219,58 @@ __device__ __forceinline__ bool walk_line(const LineArgs& a, Cut cut, const Line
   const unsigned grid = gridDim.x;
   const int lane = lane_id();
   const bool waves = sums.keys * a.pd.Hkv * (2 * a.pd.d * a.pd.elem) > kWaveBytes;
-  const bool small = sums.parts <= (int64_t)grid && !waves;
-  const int64_t total = small ? sums.parts * kSlotLen : sums.line - (waves ? sums.wave : 0);
+  *rec = make_int4(0, 0, 0, 0);
+
+  // Small calls: items of up to `whole` key tiles are not cut, longer ones into parts of
+  // about `part` tiles, when that makes no more pieces than there are CTAs: one piece to
+  // a CTA, the parts of an item to neighbours.
+  if (sums.parts <= (int64_t)grid && !waves) {
+    int before = 0;
+    for (int s0 = 0; s0 < a.pd.N; s0 += 32) {
+      if (s0 > 0) cut = cut_of<KB>(a, s0 + lane, false);
+      const int parts = parts_of(a, cut), mine = parts * cut.items * a.groups;
+      int inc = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(FULL, inc, o);
+        if (lane >= o) inc += x;
+      }
+      const unsigned m = __ballot_sync(FULL, before + inc > (int)blockIdx.x);
+      if (m == 0) {
+        before += __shfl_sync(FULL, inc, 31);
+        continue;
+      }
+      const int l = __ffs(m) - 1;
+      const unsigned np = __shfl_sync(FULL, (unsigned)parts, l);
+      const unsigned items = __shfl_sync(FULL, (unsigned)cut.items, l);
+      unsigned r = blockIdx.x - (unsigned)(before + __shfl_sync(FULL, inc - mine, l));
+      const int j = (int)(r % np);
+      r /= np;
+      Piece pc = item_piece<KB>(a, s0 + l, __shfl_sync(FULL, cut.q0, l), __shfl_sync(FULL, cut.ql, l),
+                                __shfl_sync(FULL, cut.kv, l), __shfl_sync(FULL, cut.ipt, l),
+                                (int)(r / items), (int)(r % items));
+      const int n = pc.n, len = (int)((unsigned)(n + np - 1) / np);
+      const int t0 = min(n, j * len), t1 = min(n, t0 + len);
+      if (n == 0 ? j > 0 : t1 == t0) return true;
+      pc.tb += t0;
+      pc.n = t1 - t0;
+      if (pc.n < n) {
+        pc.slot = 2 * blockIdx.x + (j > 0 ? 0 : 1);
+        if (j == 0) *rec = make_int4(pc.row0, pc.ntok, pc.g, (n + len - 1) / len);
+      }
+      return publish(pc);
+    }
+    return true;
+  }
+
+  const int64_t total = sums.line - (waves ? sums.wave : 0);
   const int64_t snap_share = (int64_t)kSnapTiles * KB * kWtDouble;
   int64_t share = (total + grid - 1) / grid;
   if (share < kLeastTiles * KB * kWtSingle) share = kLeastTiles * KB * kWtSingle;
-  if (small) {
-    share = kSlotLen;
-    if (cut.items > 0) cut_small(a, cut);
-  }
   bool ok = true;
   int held = 0;  // the 32 requests this warp's lanes hold
   auto hold = [&](int s0) {
-    if (held != s0) {
-      cut = cut_of<KB>(a, s0 + lane, false);
-      if (small && cut.items > 0) cut_small(a, cut);
-    }
+    if (held != s0) cut = cut_of<KB>(a, s0 + lane, false);
     held = s0;
   };
   // items that go in waves, all KV groups of a request together
@@ -272,7 +297,6 @@ __device__ __forceinline__ bool walk_line(const LineArgs& a, Cut cut, const Line
   // this CTA's range of the line
   const int64_t from = share * blockIdx.x;
   const int64_t to = min(total, from + share);
-  *rec = make_int4(0, 0, 0, 0);
   int64_t base = 0;  // the place of the 32 requests
   for (int s0 = 0; ok && s0 < a.pd.N && base < to; s0 += 32) {
     hold(s0);
@@ -318,9 +342,9 @@ __device__ __forceinline__ bool walk_line(const LineArgs& a, Cut cut, const Line
         const int n = pc.n;
         auto tiles_before = [&](int64_t x) -> int {  // places before x, ends snapped
           if (x <= at) return 0;
-          if (x - at >= cost) return n;
+          if (x - at >= cost || a.uncut) return n;  // (uncut: with its first tile)
           const int t = (int)min((unsigned)n, ((unsigned)(x - at) + tw - 1) / tw);
-          return share < snap_share || small ? t : t <= kSnap ? 0 : t >= n - kSnap ? n : t;
+          return share < snap_share ? t : t <= kSnap ? 0 : t >= n - kSnap ? n : t;
         };
         const int t0 = tiles_before(from), t1 = tiles_before(to);
         if (n == 0 ? at >= from : t1 > t0) {
@@ -360,7 +384,8 @@ __global__ void __launch_bounds__(NT) k_paged_merge(const __grid_constant__ Line
   __shared__ int ends[GRID];  // rows of the items up to and with c
   __shared__ int warp_sum[NT / 32];
   const int tid = threadIdx.x, lane = tid & 31;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  pdl_next();
+  pdl_wait();
   int4 r = make_int4(0, 0, 0, 0);
   if (tid < GRID) r = a.rec[tid];
   int inc = r.w > 1 ? r.y * a.heads : 0;
@@ -433,20 +458,12 @@ __global__ void __launch_bounds__(NT) k_paged_merge(const __grid_constant__ Line
 }
 
 
-// The merge, scheduled while the attention drains; it waits for the attention's end.
+// The merge (none when no item can be cut).
 template <typename E, int D, int GRID, int NT>
 int launch_merge(const LineArgs& a, E* O, float* lse, cudaStream_t st) {
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * 152);
-  cfg.blockDim = dim3(NT);
-  cfg.stream = st;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  if (a.uncut) return SGQA_OK;
   log_begin(SGQA_K_PAGED_ATTN, st);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, k_paged_merge<E, D, GRID, NT>, a, O, lse);
+  const cudaError_t e = launch_pdl(k_paged_merge<E, D, GRID, NT>, 2 * 152, NT, 0, st, a, O, lse);
   log_end(st);
   return e == cudaSuccess ? SGQA_OK : SGQA_ERR_CUDA;
 }
