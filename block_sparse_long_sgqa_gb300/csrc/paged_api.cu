@@ -16,7 +16,7 @@ int derive_paged(const sgqa_paged_params* p, PagedDims* pd) {
   if (p->dtype < 0 || p->dtype > 1 || p->causal < 0 || p->causal > 1 || p->window < 0 ||
       (p->window > 0 && !p->causal))
     return SGQA_ERR_INVALID_ARG;
-  if (!(p->softmax_scale >= 0.0f) || !std::isfinite(p->softmax_scale))
+  if (!(p->softmax_scale >= 0.0f) || !std::isfinite(p->softmax_scale * 1.4426950408889634f))
     return SGQA_ERR_INVALID_ARG;
   const int64_t hd = (int64_t)p->n_q_heads * p->head_dim;
   const int64_t kd = (int64_t)p->n_kv_heads * p->head_dim;
@@ -24,7 +24,8 @@ int derive_paged(const sgqa_paged_params* p, PagedDims* pd) {
   if ((p->q_stride != 0 && p->q_stride < hd) || (p->kv_stride != 0 && p->kv_stride < kd))
     return SGQA_ERR_INVALID_ARG;
   if (p->page_size % 8 || p->n_q_heads / p->n_kv_heads > 128 || p->max_tokens > (1 << 24) ||
-      (int64_t)p->max_pages * p->page_size > (int64_t(1) << 30) ||
+      (int64_t)p->max_pages * p->page_size > (int64_t(1) << 25) ||
+      (int64_t)p->max_tokens * p->n_q_heads > 0x7fffffffll ||
       (double)p->n_pages * p->n_kv_heads * p->page_size > 2147483647.0)
     return SGQA_ERR_UNSUPPORTED;
   pd->N = p->n_seqs;

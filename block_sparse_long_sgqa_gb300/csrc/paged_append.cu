@@ -1,4 +1,6 @@
-// New K and V rows into the paged pool through the slot map.
+// New K and V rows into the paged pool through the slot map: a copy, bound by
+// memory.  131072 rows of 8 heads of 128 in bf16: 160 us, 6.7 TB/s read and written
+// together, the rate of a plain copy; 256 rows: 2.1 us in a row of such calls.
 #include "paged.h"
 
 namespace sgqa {

@@ -17,6 +17,13 @@
 // gcd(page size, 128) rows, one lane each); 3 issues the products; 4-7 and 8-11
 // are the softmax groups, one thread per row, and write the outputs.  All rings
 // run on across pieces, so the next piece's keys load during the current one.
+//
+// What bounds it.  Single tokens over long caches: the bytes of K and V (1M keys of 8
+// heads in 600 us, 7.2 TB/s; 64 ragged contexts in 363 us, 6.8 TB/s).  Chunks: the
+// chain of a group from S to P to the products that give the next S, 2970 cycles for
+// the 2 x 1050 that the products of both groups take (4096 tokens over 36K keys, 64
+// heads: 3.05 ms, 1530 TFLOP/s; the tensor pipe is 66 % active).  Short pieces (a
+// window of 512 keys): their beginning and end, about as long as their 5 key tiles.
 #include "paged_line.cuh"
 
 namespace sgqa {
@@ -856,8 +863,8 @@ int launch_paged_tc(const PagedDims& pd, const PagedAttnArgs& pa, void* ws, cuda
   a.tpm = BM / pd.G;
   a.tiles_per_item = 2;
   a.tile_rows = BM;
-  // 0.6 us a tile: four short contexts 16.8 us, one of 8K keys 23.2 (12 and 4: 17.2
-  // and 25.5; 8 and 8: 18.0 and 23.4; cut evenly over all CTAs: 20.0 and 27.4)
+  // 0.8 us a tile: four contexts of 300 to 2047 keys 16.8 us, one of 8K 22.3 (8 and 4:
+  // 17.4 and 24.0; 8 and 8: 17.2 and 21.9; cut evenly over all CTAs: 20.0 and 27.4)
   a.whole = 8;
   a.part = 6;
   a.uncut = pd.cap <= a.whole * KB;

@@ -380,8 +380,10 @@ SGQA_API int sgqa_decode(const sgqa_params* p, const void* Q, const void* K, con
  * q_start[N] on are padding.
  * Supported: head_dim 64 and 128, page_size a multiple of 8, n_q_heads /
  * n_kv_heads up to 128, max_tokens up to 2^24, max_pages * page_size up to
- * 2^30 positions, n_pages * n_kv_heads * page_size below 2^31
- * (SGQA_ERR_UNSUPPORTED otherwise). */
+ * 2^25 positions, n_pages * n_kv_heads * page_size and max_tokens * n_q_heads
+ * below 2^31 (SGQA_ERR_UNSUPPORTED otherwise).  A call may be scheduled while
+ * the one before it on its stream ends; it touches memory only once that one
+ * is complete. */
 typedef struct sgqa_paged_params {
   int32_t n_seqs;       /* N >= 0 */
   int32_t max_tokens;   /* rows of Q, K, V, O, slot_map and positions, >= 0 */
@@ -453,10 +455,11 @@ SGQA_API int sgqa_paged_append(const sgqa_paged_params* p, const void* K, const 
  * also j > pos(t) - window.  O [max_tokens][H][d]; lse [H][max_tokens] fp32,
  * the natural log of the softmax denominator.  A token that sees nothing (a
  * position below 0, an empty cache) gets O = 0 and lse = -inf; padding rows
- * of O and lse are not written.  Positions from kv_len on, and positions no
- * row of a 128-row query tile can see because of the window, are never read
- * or have no effect whatever they hold, and neither do page_table entries of
- * pages that hold only such positions.  bf16 runs on the tensor cores (fp32
+ * of O and lse are not written.  Positions from kv_len on, and positions that
+ * no row of an item (up to 256 neighbouring (token, head) rows) can see, have
+ * no effect whatever they hold, and neither do page_table entries of pages
+ * that hold only such positions.  A key or value that some rows of an item
+ * see and others do not must be finite: 0 times a NaN is one.  bf16 runs on the tensor cores (fp32
  * softmax and accumulation, the softmax weights rounded to bf16 for their
  * product with V); fp32 runs in fp32 throughout.
  * Device checks (SGQA_ERR_BOUNDS): kv_len outside [0, max_pages * page_size]

@@ -59,7 +59,9 @@ BAD_PARAMS = [
     (dict(q_stride=8), "INVALID_ARG"), (dict(kv_stride=-128), "INVALID_ARG"),
     (dict(head_dim=96), "UNSUPPORTED"), (dict(page_size=12), "UNSUPPORTED"),
     (dict(n_q_heads=258), "UNSUPPORTED"), (dict(max_tokens=(1 << 24) + 1), "UNSUPPORTED"),
-    (dict(max_pages=1 << 27), "UNSUPPORTED"), (dict(n_pages=1 << 27), "UNSUPPORTED"),
+    (dict(softmax_scale=3e38), "INVALID_ARG"),
+    (dict(max_pages=(1 << 21) + 1), "UNSUPPORTED"),
+    (dict(max_tokens=1 << 20, n_q_heads=2048, n_kv_heads=16), "UNSUPPORTED"), (dict(n_pages=1 << 27), "UNSUPPORTED"),
     (dict(q_stride=513), "ALIGNMENT"), (dict(kv_stride=130), "ALIGNMENT"),
 ]
 
@@ -646,6 +648,37 @@ def test_attention_graphs_share_a_workspace(s, dtype):
             O2, l2 = torch.full_like(O, 3.0), torch.full_like(lse, 7.0)
             s.sgqa_paged_attn(p, **t, O=O2, lse=l2, ws=s.alloc_paged_workspace(p))
             assert torch.equal(O, O2) and torch.equal(lse, l2), it
+
+
+@gpu
+def test_attention_captured_behind_copies(s):
+    """A captured step whose inputs come by copies and fills inside the graph."""
+    b, p, wide, K, V, q_start, kw = attn_case(s, "chunk", "bf16")
+    src = [wide.cuda(), dev(b.kv)]
+    Q, kv = torch.zeros_like(src[0]), torch.zeros_like(src[1])
+    Kd, Vd, pt, qs = K.cuda(), V.cuda(), dev(b.table), dev(q_start)
+    O = torch.zeros_like(Q)
+    lse = torch.zeros(p.n_q_heads, p.max_tokens, device="cuda")
+    ws = s.alloc_paged_workspace(p)
+
+    def step():
+        Q.copy_(src[0])
+        kv.copy_(src[1])
+        O.zero_()
+        s.sgqa_paged_attn(p, Q, Kd, Vd, pt, qs, kv, O, lse, ws)
+        Q.zero_()
+        kv.zero_()
+
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for _ in range(5):
+        O.fill_(9.0)
+        lse.fill_(9.0)
+        g.replay()
+        check_attn(s, b, p, wide, K, V, q_start, kw, O, lse)
 
 
 @gpu
