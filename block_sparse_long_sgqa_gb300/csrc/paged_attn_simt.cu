@@ -24,8 +24,10 @@ constexpr int KT = 64;  // keys per tile
 constexpr int NT = 256;
 constexpr int LPR = NT / KT;  // threads that load a row of a tile
 
-template <int D, int RPT>
+constexpr int RPT = 4;
+template <int D>
 struct Cfg {
+  static constexpr int NTH = NT, KB = KT;
   static constexpr int R = NT / 16 * RPT;
   static constexpr int PER_SM = 2, GRID = 152 * PER_SM;  // (three of d = 64: registers spill)
   static constexpr int QS = D + 4;   // row strides in shared memory (floats): the
@@ -53,9 +55,9 @@ __device__ __forceinline__ void copy16(float* dst, const float* src, bool on) {
                : "memory");
 }
 
-template <int D, int RPT>
+template <int D>
 __device__ __noinline__ void simt_piece(const SimtArgs& a, const Piece pc, float* sm) {
-  using C = Cfg<D, RPT>;
+  using C = Cfg<D>;
   constexpr int R = C::R, DC = D / 64;
   float* sQ = sm;
   float* sK = sQ + R * C::QS;
@@ -238,44 +240,303 @@ __device__ __noinline__ void simt_piece(const SimtArgs& a, const Piece pc, float
   }
 }
 
-template <int D, int RPT>
-__global__ void __launch_bounds__(NT, (Cfg<D, RPT>::PER_SM))
-    k_paged_simt(const __grid_constant__ SimtArgs a) {
-  extern __shared__ __align__(16) float sm[];
-  __shared__ int64_t warp_sums[NT / 32][4];
+// Few rows (R = 8 or 16: single tokens of a group of that many heads): the products are
+// small and the bytes of K and V count, so the warps share nothing.  Of each tile a warp
+// takes 8 keys for itself: it copies their K and V a tile ahead, and keeps a maximum, a
+// sum and an output of its own for all R rows; the warps' are joined at the piece's end.
+// No barrier inside a piece.  S: a lane sums 4 rows x 4 keys over one of NS parts of the
+// columns; the parts are added and dealt out by halves, so that the lane ends with KL
+// keys of one row.  O: a lane has 4 columns of every row (d = 64: of every other R / 2).
+// What bounds it is reads of shared memory and instructions beside the copies: 16
+// requests of 3000 keys, 32 on 4 heads of 128, 55 us against 129 with the tiles above
+// (195 MB: 29 us); two of 110000 keys 173 us against 514 (0.90 GB: 133 us).  One row and
+// two keys a lane, with no sum over lanes: 70 us; 8 warps of d = 128 for 12: 58 us;
+// three stages for two: 2 us more; P stored in pairs, for fewer moves: 2 us more.
+template <int D, int R_>
+struct Few {
+  static constexpr int R = R_, NTH = D == 128 ? 384 : 256, WARPS = NTH / 32, WK = 8, STAGES = 2;
+  static constexpr int KB = WARPS * WK;                         // keys of a tile
+  static constexpr int KL = WK * R / 32, NS = 128 / R * 4 / WK;
+  static constexpr int PER_SM = D == 128 ? 1 : 2, GRID = 152 * PER_SM;
+  static constexpr int QS = D + 4, KS = D;  // rows 4 apart: 16 banks apart
+  static constexpr int STAGE = WK * (KS + D);                  // floats of a warp's stage
+  static constexpr int WARP = STAGES * STAGE + WK * R + 2 * R;  // + P, maxima and sums
+  static constexpr int SMEM = (R * QS + WARPS * WARP) * 4;
+  static constexpr int RO = D == 128 ? R : R / 2;              // rows of O in a lane
+  static_assert(STAGES * STAGE >= R * D, "O lies over the stages at the end");
+  static_assert(WARP % 4 == 0 && KL * 32 == WK * R && WK == 8 && (NS == 8 || NS == 4), "");
+};
+
+template <int D, int R>
+__device__ __noinline__ void few_piece(const SimtArgs& a, const Piece pc, float* sm) {
+  using F = Few<D, R>;
+  constexpr int KL = F::KL, NS = F::NS;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int split = lane % NS, rt = lane / NS % (R / 4), kt = lane >> 4;
+  const int row = rt * 4 + split / (NS / 4), key0 = kt * 4 + (NS == 8 ? (split & 1) * 2 : 0);
+  // over the lanes that have the same row
+  auto row_max = [](float x) {
+    x = fmaxf(x, __shfl_xor_sync(FULL, x, 16));
+    return NS == 8 ? fmaxf(x, __shfl_xor_sync(FULL, x, 1)) : x;
+  };
+  auto row_sum = [](float x) {
+    x += __shfl_xor_sync(FULL, x, 16);
+    return NS == 8 ? x + __shfl_xor_sync(FULL, x, 1) : x;
+  };
+  float* sQ = sm;
+  float* mine = sm + R * F::QS + warp * F::WARP;
+  float* sP = mine + F::STAGES * F::STAGE;
+  float* sM = sP + F::WK * R;
+  const int h0 = first_head(a, pc.g), nh = heads_of(a, pc.g), rows = pc.ntok * a.heads;
+  const int kvh = pc.g / a.head_parts;
+  const float ninf = -__int_as_float(0x7f800000);
+
+  __syncthreads();  // the last piece's outputs have been read
+  for (int i = tid; pc.n > 0 && i < R * (D / 4); i += F::NTH) {
+    const int r = i / (D / 4), c = i % (D / 4) * 4;
+    const int tok = r / a.heads, h = r - tok * a.heads;
+    const bool on = r < rows && h < nh;
+    copy16(sQ + r * F::QS + c, a.Q + (on ? (pc.row0 + tok) * a.pd.qs + (int64_t)(h0 + h) * D + c : 0), on);
+  }
+  asm volatile("cp.async.commit_group;" ::: "memory");
+  // The warp's keys of a tile are copied row by row, so that an instruction reads whole
+  // lines.  Lane i looks up the page of key i (mod WK), a tile before its copy.
+  const int first = pc.tb * F::KB + warp * F::WK;
+  auto key_of = [&](int t) { return first + t * F::KB + lane % F::WK; };
+  auto page_of = [&](int t) {
+    const int key = key_of(t);
+    return t < pc.n && key >= pc.lo && key < pc.hi
+               ? a.page_table[(int64_t)pc.s * a.pd.max_pages + key / a.pd.ps]
+               : -1;
+  };
+  auto load = [&](int t, int page) {
+    if (t < pc.n) {
+      float* sK = mine + t % F::STAGES * F::STAGE;
+      float* sV = sK + F::WK * F::KS;
+      const int key = key_of(t);
+      int64_t at = -1;
+      if (page >= 0 && page < a.pd.n_pages)
+        at = ((int64_t)page * a.pd.Hkv + kvh) * a.pd.ps + key % a.pd.ps;
+      else if (lane < F::WK && key >= pc.lo && key < pc.hi)
+        report(a.status, SGQA_ERR_BOUNDS, 302);
+      constexpr int LPK = D / 4;  // lanes of a key
+#pragma unroll
+      for (int i = 0; i < F::WK; i += 32 / LPK) {
+        const int kr = i + lane / LPK, c = lane % LPK * 4;
+        const int64_t from = __shfl_sync(FULL, at, kr);
+        const bool on = from >= 0;
+        copy16(sK + kr * F::KS + c, a.K + (on ? from * D + c : 0), on);
+        copy16(sV + kr * D + c, a.V + (on ? from * D + c : 0), on);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  load(0, page_of(0));
+  int page = page_of(1);
+  asm volatile("cp.async.wait_group 1;" ::: "memory");
+  __syncthreads();  // Q is there
+
+  const int pos = pc.pos0 + row / a.heads;
+  const int end = a.pd.causal ? min(pc.hi, pos + 1) : pc.hi;
+  const int beg = a.pd.window ? max(pc.lo, pos + 1 - a.pd.window) : pc.lo;
+  float m = ninf, l = 0.f;  // of `row`; l: over this lane's keys
+  uint64_t o[F::RO][2];
+#pragma unroll
+  for (int i = 0; i < F::RO; ++i) o[i][0] = o[i][1] = 0ull;
+  const int oc = D == 128 ? lane * 4 : lane % 16 * 4;       // columns of O
+  const int or0 = D == 128 ? 0 : lane / 16 * F::RO;             // and its first row
+  for (int t = 0; t < pc.n; ++t) {
+    load(t + 1, page);
+    page = page_of(t + 2);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    __syncwarp();
+    const float* sK = mine + t % F::STAGES * F::STAGE;
+    const float* sV = sK + F::WK * F::KS;
+    float x[16];
+    {
+      uint64_t s2[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s2[e] = 0ull;
+#pragma unroll
+      for (int c = split * 4; c < D; c += NS * 4) {
+        ulonglong2 q[4], k[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          q[i] = *reinterpret_cast<const ulonglong2*>(sQ + (rt * 4 + i) * F::QS + c);
+          k[i] = *reinterpret_cast<const ulonglong2*>(sK + (kt * 4 + i) * F::KS + c);
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          s2[e] = f2_fma(q[e / 4].x, k[e % 4].x, s2[e]);
+          s2[e] = f2_fma(q[e / 4].y, k[e % 4].y, s2[e]);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        float even, odd;
+        f2_unpack(s2[e], even, odd);
+        x[e] = even + odd;
+      }
+    }
+#pragma unroll
+    for (int n = 8, to = NS / 2; to > 0; n >>= 1, to >>= 1) {
+      const bool hi = split & to;
+#pragma unroll
+      for (int e = 0; e < n; ++e)
+        x[e] = (hi ? x[e + n] : x[e]) + __shfl_xor_sync(FULL, hi ? x[e] : x[e + n], to);
+    }
+    const int k0 = first + t * F::KB + key0;
+    float p[KL], mx = ninf;
+#pragma unroll
+    for (int j = 0; j < KL; ++j) {
+      p[j] = k0 + j >= beg && k0 + j < end ? x[j] * a.sl2 : ninf;
+      mx = fmaxf(mx, p[j]);
+    }
+    mx = row_max(mx);
+    // the maximum is raised, and O rescaled, only when it is exceeded by 2^8: fp32
+    // holds weights up to that with the precision of weights up to 1
+    const bool raise = mx > m + 8.f;
+    if (__any_sync(FULL, raise)) {
+      const float f = raise ? ex2(m - mx) : 1.f;
+      l *= f;
+      if (raise) m = mx;
+#pragma unroll
+      for (int i = 0; i < F::RO; ++i) {
+        const float fr = __shfl_sync(FULL, f, (or0 + i) * (NS / 4));
+        o[i][0] = f2_mul(o[i][0], f2_pack(fr, fr));
+        o[i][1] = f2_mul(o[i][1], f2_pack(fr, fr));
+      }
+    }
+    const float base = m == ninf ? 0.f : m;
+#pragma unroll
+    for (int j = 0; j < KL; ++j) {
+      p[j] = ex2(p[j] - base);
+      l += p[j];
+      sP[(key0 + j) * R + row] = p[j];
+    }
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < F::WK; ++k) {
+      const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(sV + k * D + oc);
+#pragma unroll
+      for (int i = 0; i < F::RO; i += 4) {
+        const float4 w = *reinterpret_cast<const float4*>(sP + k * R + or0 + i);
+        const float we[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          o[i + e][0] = f2_fma(f2_pack(we[e], we[e]), v.x, o[i + e][0]);
+          o[i + e][1] = f2_fma(f2_pack(we[e], we[e]), v.y, o[i + e][1]);
+        }
+      }
+    }
+    __syncwarp();  // P and this stage are written again two steps on
+  }
+
+  // ---- the warps' parts joined
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < F::RO; ++i) {
+    float4 v;
+    f2_unpack(o[i][0], v.x, v.y);
+    f2_unpack(o[i][1], v.z, v.w);
+    *reinterpret_cast<float4*>(mine + (or0 + i) * D + oc) = v;
+  }
+  l = row_sum(l);
+  if (key0 == 0) {
+    sM[row] = m;
+    sM[R + row] = l;
+  }
+  __syncthreads();
+  for (int i = tid; i < R * (D / 4); i += F::NTH) {
+    const int r = i / (D / 4), c0 = i % (D / 4) * 4;
+    const int tok = r / a.heads, h = r - tok * a.heads;
+    if (r >= rows || h >= nh) continue;
+    const float* warp0 = sm + R * F::QS;
+    const float* stats = warp0 + F::STAGES * F::STAGE + F::WK * R + r;
+    float mm = ninf, lt = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < F::WARPS; ++w) mm = fmaxf(mm, stats[w * F::WARP]);
+#pragma unroll
+    for (int w = 0; w < F::WARPS; ++w) {
+      const float mw = stats[w * F::WARP];
+      const float f = mw == ninf ? 0.f : ex2(mw - mm);
+      const float4 v = *reinterpret_cast<const float4*>(warp0 + w * F::WARP + r * D + c0);
+      lt = fmaf(f, stats[w * F::WARP + R], lt);
+      acc.x = fmaf(f, v.x, acc.x);
+      acc.y = fmaf(f, v.y, acc.y);
+      acc.z = fmaf(f, v.z, acc.z);
+      acc.w = fmaf(f, v.w, acc.w);
+    }
+    const int64_t t = pc.row0 + tok, hq = h0 + h;
+    const float inv = lt > 0.f ? 1.f / lt : 0.f;
+    const int64_t slot_row = (int64_t)pc.slot * a.slot_rows + r;
+    float* dst = pc.slot >= 0 ? a.opart + slot_row * D : a.O + (t * a.pd.H + hq) * D;
+    *reinterpret_cast<float4*>(dst + c0) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    if (c0 == 0) {
+      const float lse = lt > 0.f ? (mm + log2f(lt)) * 0.69314718055994531f : ninf;
+      (pc.slot >= 0 ? a.lpart[slot_row] : a.lse[hq * a.pd.T + t]) = lse;
+    }
+  }
+}
+
+// The CTA's pieces: every warp walks the line, so that none has to be told.
+template <typename C, typename Work>
+__device__ __forceinline__ void simt_pieces(const SimtArgs& a, Work work) {
+  constexpr int KB = C::KB, N = C::NTH;
+  __shared__ int64_t warp_sums[N / 32][4];
   pdl_next();
   pdl_wait();
   {
-    const Cut mine = cut_of<KT>(a, threadIdx.x, blockIdx.x == 0);
-    line_sums<KT, NT>(a, mine, warp_sums);
+    const Cut mine = cut_of<KB>(a, threadIdx.x, blockIdx.x == 0);
+    line_sums<KB, N>(a, mine, warp_sums);
   }
   __syncthreads();
-  const LineSums sums = add_sums<NT>(a, warp_sums);
+  const LineSums sums = add_sums<N>(a, warp_sums);
   int4 rec;
-  walk_line<KT>(a, cut_of<KT>(a, (int)lane_id(), false), sums,
+  walk_line<KB>(a, cut_of<KB>(a, (int)lane_id(), false), sums,
                 [&](const Piece& pc) {
-                  simt_piece<D, RPT>(a, pc, sm);
+                  work(pc);
                   return true;
                 },
                 &rec);
   if (threadIdx.x == 0) a.rec[blockIdx.x] = rec;
 }
 
-// Rows per item: 16 when the requests have on average at most that many (one token
-// each, a group of up to 16 heads), else 64.
-int grid_of(const PagedDims& pd) { return pd.d == 128 ? Cfg<128, 4>::GRID : Cfg<64, 4>::GRID; }
-int rows_per_item(const PagedDims& pd) {
-  return (int64_t)pd.T * pd.G <= (int64_t)16 * pd.N ? 16 : 64;
+template <int D>
+__global__ void __launch_bounds__(NT, (Cfg<D>::PER_SM)) k_paged_simt(const __grid_constant__ SimtArgs a) {
+  extern __shared__ __align__(16) float sm[];
+  simt_pieces<Cfg<D>>(a, [&](const Piece& pc) { simt_piece<D>(a, pc, sm); });
+}
+template <int D, int R>
+__global__ void __launch_bounds__((Few<D, R>::NTH), (Few<D, R>::PER_SM))
+    k_paged_few(const __grid_constant__ SimtArgs a) {
+  extern __shared__ __align__(16) float sm[];
+  simt_pieces<Few<D, R>>(a, [&](const Piece& pc) { few_piece<D, R>(a, pc, sm); });
 }
 
-template <int D, int RPT>
-int launch(const SimtArgs& a, cudaStream_t st) {
-  using C = Cfg<D, RPT>;
-  if (cudaFuncSetAttribute(k_paged_simt<D, RPT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           C::SMEM) != cudaSuccess)
+// Rows per item: 8 or 16 when the requests have on average at most that many and a group
+// fits (one token each: 55 and 129 us for 16 requests of 3000 keys, see above), else 64.
+int rows_of(const PagedDims& pd) {
+  for (int R : {8, 16})
+    if (pd.G <= R && (int64_t)pd.T * pd.G <= (int64_t)R * pd.N) return R;
+  return 64;
+}
+int grid_of(const PagedDims& pd) {
+  static_assert(Few<128, 8>::GRID == Few<128, 16>::GRID && Few<64, 8>::GRID == Few<64, 16>::GRID, "");
+  if (rows_of(pd) <= 16) return pd.d == 128 ? Few<128, 16>::GRID : Few<64, 16>::GRID;
+  return pd.d == 128 ? Cfg<128>::GRID : Cfg<64>::GRID;
+}
+
+template <typename C, int D>
+int launch(void (*kernel)(SimtArgs), SimtArgs& a, cudaStream_t st) {
+  a.uncut = a.pd.cap <= a.whole * C::KB;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
+      cudaSuccess)
     return SGQA_ERR_CUDA;
   log_begin(SGQA_K_PAGED_ATTN, st);
-  const cudaError_t e = launch_pdl(k_paged_simt<D, RPT>, C::GRID, NT, C::SMEM, st, a);
+  const cudaError_t e = launch_pdl(kernel, C::GRID, C::NTH, C::SMEM, st, a);
   log_end(st);
   if (e != cudaSuccess) return SGQA_ERR_CUDA;
   return launch_merge<float, D, C::GRID, (C::GRID + 31) / 32 * 32>(a, a.O, a.lse, st);
@@ -284,11 +545,11 @@ int launch(const SimtArgs& a, cudaStream_t st) {
 }  // namespace
 
 size_t paged_simt_ws_bytes(const PagedDims& pd) {
-  return pd.N == 0 || pd.T == 0 ? 0 : carve_line(grid_of(pd), rows_per_item(pd), pd.d).bytes;
+  return pd.N == 0 || pd.T == 0 ? 0 : carve_line(grid_of(pd), rows_of(pd), pd.d).bytes;
 }
 
 int launch_paged_simt(const PagedDims& pd, const PagedAttnArgs& pa, void* ws, cudaStream_t st) {
-  const int R = rows_per_item(pd);
+  const int R = rows_of(pd);
   SimtArgs a;
   a.slot_rows = R;
   set_line(a, pd, pa, carve_line(grid_of(pd), R, pd.d), ws);
@@ -298,9 +559,8 @@ int launch_paged_simt(const PagedDims& pd, const PagedAttnArgs& pa, void* ws, cu
   a.tpm = R / a.heads;
   a.tiles_per_item = 1;
   a.tile_rows = 0;
-  // 2 to 3 us a tile: four contexts of up to 700 keys 22.7 us (2 and 1: 30.0, 4 and 2: 31.2)
+  // four contexts of up to 700 keys 16.5 us (whole = 2: 18.4)
   a.whole = a.part = 1;
-  a.uncut = pd.cap <= a.whole * KT;
   a.Q = static_cast<const float*>(pa.Q);
   a.K = static_cast<const float*>(pa.K);
   a.V = static_cast<const float*>(pa.V);
@@ -309,8 +569,14 @@ int launch_paged_simt(const PagedDims& pd, const PagedAttnArgs& pa, void* ws, cu
   a.sl2 = pd.scale * 1.4426950408889634f;
   // whole items of a request, over its groups, are counted in 32 bits
   if ((int64_t)a.groups * ((int64_t)pd.T / a.tpm + 1) > 0x7fffffffll) return SGQA_ERR_UNSUPPORTED;
-  if (pd.d == 128) return R == 16 ? launch<128, 1>(a, st) : launch<128, 4>(a, st);
-  return R == 16 ? launch<64, 1>(a, st) : launch<64, 4>(a, st);
+  if (R == 8)
+    return pd.d == 128 ? launch<Few<128, 8>, 128>(k_paged_few<128, 8>, a, st)
+                       : launch<Few<64, 8>, 64>(k_paged_few<64, 8>, a, st);
+  if (R == 16)
+    return pd.d == 128 ? launch<Few<128, 16>, 128>(k_paged_few<128, 16>, a, st)
+                       : launch<Few<64, 16>, 64>(k_paged_few<64, 16>, a, st);
+  return pd.d == 128 ? launch<Cfg<128>, 128>(k_paged_simt<128>, a, st)
+                     : launch<Cfg<64>, 64>(k_paged_simt<64>, a, st);
 }
 
 }  // namespace sgqa

@@ -391,6 +391,14 @@ ATTN = {
     "many_requests": ([1, 0, 1] * 150, [(7 * i) % 131 + 1 for i in range(450)], 4, 2, 64, 16, {}),
     "many_chunks": ([1, 40, 0, 17] * 20, [60 + 31 * (i % 9) for i in range(80)], 8, 2, 64, 16, {}),
     "one_head_many_tiles": ([1000], [1300], 4, 1, 64, 32, {}),
+    # few rows a request, one of them with all the tokens, two tokens an item
+    "few_g5": ([1, 1, 1], [3000, 95, 97], 20, 4, 128, 16, {}),
+    "few_g8_d64": ([1] * 5, [1, 63, 64, 65, 2000], 16, 2, 64, 8, {}),
+    "few_g16": ([1] * 4, [96, 191, 193, 2500], 32, 2, 128, 64, {}),
+    "few_g11_window": ([1, 1], [1500, 30], 22, 2, 64, 24, dict(window=70)),
+    "few_in_one_request": ([6, 0, 0, 0, 0, 0], [500, 9, 0, 3, 0, 1], 16, 2, 128, 16, {}),
+    "few_two_tokens": ([2, 2, 2], [300, 100, 2], 8, 2, 128, 40, {}),
+    "few_full": ([1, 1], [700, 0], 16, 2, 128, 16, dict(causal=False)),
 }
 
 
