@@ -6,13 +6,15 @@
 // P = 2^(S - m'), l = l 2^(m - m') + rowsum P, O = O 2^(m - m') + P V; at the end O /
 // l and lse = ln 2 (m + log2 l).  An item's rows are (token, head of the group)
 // pairs in that order, so every key read serves all of them.  256 threads as 16 x 16:
-// thread (ty, tx) holds rows RPT ty .. RPT ty + RPT - 1 and of each 64 keys tx + 16 j,
-// and of each row of O the columns 4 tx + 64 c.  Products in the packed f32x2 form: a
-// warp's 64 FMAs in 2.0 cycles, against 2 x 1.2 for the scalar one.  What bounds it is
-// shared memory: a 4 x 4 tile of S needs 12 wavefronts of reads for 64 cycles of FMAs,
-// three quarters of what the SM's four schedulers leave room for (measured: the FMA
-// pipe 48 % busy, shared memory 70 %).  An 8 x 4 tile needs half, but leaves 8 warps
-// an SM and was slower (2882 us against 2563 on 2656 tokens of 32 heads).
+// thread (ty, tx) holds rows 4 ty .. 4 ty + 3 and of each 64 keys tx + 16 j, and of each
+// row of O the columns 4 tx + 64 c.  V is copied while S is formed and the next K while
+// P V is, so a tile has two barriers and waits for neither; a row of P stays within its
+// warp.  Products in the packed f32x2 form: a warp's 64 FMAs in 2.0 cycles, against 2 x
+// 1.2 for the scalar one.  What bounds it: the FMA pipe is 60 % busy and shared memory 74
+// % (3.1 wavefronts a read) with four warps a scheduler, which registers and shared memory
+// both allow and no more: 2656 tokens of 32 heads of 128 on contexts of 500 to 3000 keys
+// 2367 us, 38 of the 74 TFLOP/s of the pipe.  8 rows a thread halves the reads but leaves
+// two warps a scheduler: 2637 us.  K and V copied at the tile's start: 70 us more.
 // paged_line.cuh lays the work out over two CTAs per SM; every warp walks it,
 // so that a CTA needs no hand-over between its warps.
 #include "paged_line.cuh"
@@ -23,18 +25,16 @@ namespace {
 constexpr int KT = 64;  // keys per tile
 constexpr int NT = 256;
 constexpr int LPR = NT / KT;  // threads that load a row of a tile
+constexpr int RPT = 4;        // rows of a thread
 
-constexpr int RPT = 4;
 template <int D>
 struct Cfg {
   static constexpr int NTH = NT, KB = KT;
   static constexpr int R = NT / 16 * RPT;
   static constexpr int PER_SM = 2, GRID = 152 * PER_SM;  // (three of d = 64: registers spill)
-  static constexpr int QS = D + 4;   // row strides in shared memory (floats): the
-  static constexpr int KS = D + 4;   // 16-byte reads of 8 neighbouring rows fall in
-  static constexpr int PS = KT + 4;  // different banks
-  static_assert(R * PS <= KT * KS, "P lies over K");
-  static constexpr int SMEM = (R * QS + KT * KS + KT * D) * 4;
+  static constexpr int QS = D * RPT + 4;  // RPT rows of Q (their reads: 4 banks apart)
+  static constexpr int SMEM = (R / RPT * QS + 2 * KT * D + R * KT) * 4;
+  static_assert(PER_SM * (SMEM + 1024 + NT) <= 228 * 1024, "two CTAs fit an SM");
 };
 
 struct SimtArgs : LineArgs {
@@ -60,10 +60,11 @@ __device__ __noinline__ void simt_piece(const SimtArgs& a, const Piece pc, float
   using C = Cfg<D>;
   constexpr int R = C::R, DC = D / 64;
   float* sQ = sm;
-  float* sK = sQ + R * C::QS;
-  float* sP = sK;  // over K, once S is done
-  float* sV = sK + KT * C::KS;
-  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+  float* sK = sQ + R / RPT * C::QS;  // rows of 16-byte units, unit u of row r at u ^ (r & 7)
+  float* sV = sK + KT * D;
+  float* sP = sV + KT * D;           // of an odd ty: keys ^ 16
+  // a half warp is 2 ty x 8 tx: its 16-byte reads of an operand are one wavefront
+  const int tid = threadIdx.x, ty = tid / 32 * 2 + (tid >> 3 & 1), tx = (tid & 7) + (tid >> 1 & 8);
   const int h0 = first_head(a, pc.g), nh = heads_of(a, pc.g), rows = pc.ntok * a.heads;
   const int kvh = pc.g / a.head_parts;
   const float ninf = -__int_as_float(0x7f800000);
@@ -73,7 +74,7 @@ __device__ __noinline__ void simt_piece(const SimtArgs& a, const Piece pc, float
     const int r = i / (D / 4), c = i % (D / 4) * 4;
     const int tok = r / a.heads, h = r - tok * a.heads;
     const bool on = r < rows && h < nh;
-    copy16(sQ + r * C::QS + c, a.Q + (on ? (pc.row0 + tok) * a.pd.qs + (int64_t)(h0 + h) * D + c : 0), on);
+    copy16(sQ + r / RPT * C::QS + r % RPT * D + c, a.Q + (on ? (pc.row0 + tok) * a.pd.qs + (int64_t)(h0 + h) * D + c : 0), on);
   }
   float m[RPT], l[RPT];
   uint64_t o[RPT][DC][2];  // columns in pairs
@@ -90,35 +91,39 @@ __device__ __noinline__ void simt_piece(const SimtArgs& a, const Piece pc, float
   }
 
   const int kr = tid / LPR;  // the row of the tile that this thread loads a part of
+  int64_t at = -1;           // and where that row of tile t is
+  auto find = [&](int t) {
+    const int key = t * KT + kr;
+    at = -1;
+    if (key < pc.lo || key >= pc.hi) return;
+    const int pi = key / a.pd.ps;
+    const int page = a.page_table[(int64_t)pc.s * a.pd.max_pages + pi];
+    if (page >= 0 && page < a.pd.n_pages)
+      at = (((int64_t)page * a.pd.Hkv + kvh) * a.pd.ps + (key - pi * a.pd.ps)) * D;
+    else if (tid % LPR == 0)
+      report(a.status, SGQA_ERR_BOUNDS, 302);
+  };
+  auto load = [&](float* dst, const float* src, int swizzle) {
+#pragma unroll
+    for (int i = 0; i < D / 4 / LPR; ++i) {
+      const int u = tid % LPR + LPR * i;
+      copy16(dst + kr * D + (u ^ swizzle) * 4, src + (at >= 0 ? at + u * 4 : 0), at >= 0);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  const float* kRow = sK + tx * D;
+  const float* qRow = sQ + ty * C::QS;
+  float* pRow = sP + ty * RPT * KT;
+  const int psw = (ty & 1) * 16;
+  if (pc.n > 0) {
+    find(pc.tb);
+    load(sK, a.K, kr & 7);
+  }
   for (int t = pc.tb; t < pc.tb + pc.n; ++t) {
-    const int k0 = t * KT, key = k0 + kr;
-    bool on = key >= pc.lo && key < pc.hi;
-    int64_t at = 0;
-    if (on) {
-      const int pi = key / a.pd.ps;
-      const int page = a.page_table[(int64_t)pc.s * a.pd.max_pages + pi];
-      if (page >= 0 && page < a.pd.n_pages) {
-        at = (((int64_t)page * a.pd.Hkv + kvh) * a.pd.ps + (key - pi * a.pd.ps)) * D;
-      } else {
-        on = false;
-        if (tid % LPR == 0) report(a.status, SGQA_ERR_BOUNDS, 302);
-      }
-    }
-    __syncthreads();  // the last tile's P and V have been read
-#pragma unroll
-    for (int i = 0; i < D / 4 / LPR; ++i) {
-      const int c = (tid % LPR + LPR * i) * 4;
-      copy16(sK + kr * C::KS + c, a.K + at + c, on);
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < D / 4 / LPR; ++i) {
-      const int c = (tid % LPR + LPR * i) * 4;
-      copy16(sV + kr * D + c, a.V + at + c, on);
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    asm volatile("cp.async.wait_group 1;" ::: "memory");
-    __syncthreads();
+    const int k0 = t * KT;
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();  // K (and Q) are there, the last tile's V has been read
+    load(sV, a.V, 0);
     float p[RPT][4];
     {
       uint64_t q2[RPT][4];  // sums over even and odd columns
@@ -131,10 +136,10 @@ __device__ __noinline__ void simt_piece(const SimtArgs& a, const Piece pc, float
         ulonglong2 kk[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          kk[j] = *reinterpret_cast<const ulonglong2*>(sK + (tx + 16 * j) * C::KS + c);
+          kk[j] = *reinterpret_cast<const ulonglong2*>(kRow + 16 * j * D + (c ^ (tx & 7) * 4));
 #pragma unroll
         for (int i = 0; i < RPT; ++i) {
-          const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(sQ + (ty * RPT + i) * C::QS + c);
+          const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(qRow + i * D + c);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             q2[i][j] = f2_fma(q.x, kk[j].x, q2[i][j]);
@@ -151,7 +156,12 @@ __device__ __noinline__ void simt_piece(const SimtArgs& a, const Piece pc, float
           p[i][j] = x + y;
         }
     }
-    __syncthreads();  // K has been read: P may be written over it
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();  // V is there, K has been read
+    if (t + 1 < pc.tb + pc.n) {
+      find(t + 1);
+      load(sK, a.K, kr & 7);
+    }
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
       float mx = ninf;
@@ -162,7 +172,7 @@ __device__ __noinline__ void simt_piece(const SimtArgs& a, const Piece pc, float
         mx = fmaxf(mx, p[i][j]);
       }
 #pragma unroll
-      for (int x = 8; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+      for (int x : {1, 2, 4, 16}) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, x));
       const float mn = fmaxf(m[i], mx);
       const float base = mn == ninf ? 0.f : mn;  // nothing seen so far: all P are 0
       const float f = ex2(m[i] - base);
@@ -171,7 +181,7 @@ __device__ __noinline__ void simt_piece(const SimtArgs& a, const Piece pc, float
       for (int j = 0; j < 4; ++j) {
         p[i][j] = ex2(p[i][j] - base);
         sum += p[i][j];
-        sP[(ty * RPT + i) * C::PS + tx + 16 * j] = p[i][j];
+        pRow[i * KT + ((tx + 16 * j) ^ psw)] = p[i][j];
       }
       l[i] = l[i] * f + sum;  // this thread's keys; summed over tx at the end
       m[i] = mn;
@@ -182,23 +192,22 @@ __device__ __noinline__ void simt_piece(const SimtArgs& a, const Piece pc, float
         o[i][c][1] = f2_mul(o[i][c][1], ff);
       }
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    __syncthreads();
-#pragma unroll 4
-    for (int k = 0; k < KT; k += 2) {
-      float2 pr[RPT];
+    __syncwarp();  // a row of P is written and read by one warp
+#pragma unroll 8
+    for (int k = 0; k < KT; k += 4) {
+      float4 pr[RPT];
 #pragma unroll
       for (int i = 0; i < RPT; ++i)
-        pr[i] = *reinterpret_cast<const float2*>(sP + (ty * RPT + i) * C::PS + k);
+        pr[i] = *reinterpret_cast<const float4*>(pRow + i * KT + (k ^ psw));
 #pragma unroll
-      for (int kk = 0; kk < 2; ++kk) {
+      for (int kk = 0; kk < 4; ++kk) {
         ulonglong2 v[DC];
 #pragma unroll
         for (int c = 0; c < DC; ++c)
           v[c] = *reinterpret_cast<const ulonglong2*>(sV + (k + kk) * D + c * 64 + tx * 4);
 #pragma unroll
         for (int i = 0; i < RPT; ++i) {
-          const float x = kk == 0 ? pr[i].x : pr[i].y;
+          const float x = kk == 0 ? pr[i].x : kk == 1 ? pr[i].y : kk == 2 ? pr[i].z : pr[i].w;
           const uint64_t pv = f2_pack(x, x);
 #pragma unroll
           for (int c = 0; c < DC; ++c) {
@@ -215,7 +224,7 @@ __device__ __noinline__ void simt_piece(const SimtArgs& a, const Piece pc, float
     const int r = ty * RPT + i;
     float lt = l[i];
 #pragma unroll
-    for (int x = 8; x > 0; x >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, x);
+    for (int x : {1, 2, 4, 16}) lt += __shfl_xor_sync(FULL, lt, x);
     const int tok = r / a.heads, h = r - tok * a.heads;
     if (r >= rows || h >= nh) continue;
     const int64_t t = pc.row0 + tok, hq = h0 + h;
