@@ -23,7 +23,8 @@
 // chain of a group from S to P to the products that give the next S, 2970 cycles for
 // the 2 x 1050 that the products of both groups take (4096 tokens over 36K keys, 64
 // heads: 3.05 ms, 1530 TFLOP/s; the tensor pipe is 66 % active).  Short pieces (a
-// window of 512 keys): their beginning and end, about as long as their 5 key tiles.
+// window of 512 keys, 169 us): 5 of a piece's 21 thousand cycles pass between the last
+// P and the next first S, and three of its five key tiles are masked.
 #include "paged_line.cuh"
 
 namespace sgqa {
@@ -713,17 +714,21 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       vbase += pc.n;
       // ---- outputs
       const int n0 = pc.single ? (pc.n + 1) / 2 : pc.n, n1 = pc.single ? pc.n / 2 : pc.n;
-      if ((grp == 0 ? n0 : n1) > 0) {
-        ok = __all_sync(FULL, mbar_wait(&o_full[grp], (uint32_t)(oc & 1), ab, a.status, 343));
-        if (!ok) break;
+      auto o_done = [&]() -> bool {
+        if ((grp == 0 ? n0 : n1) == 0) return true;
+        const bool done =
+            __all_sync(FULL, mbar_wait(&o_full[grp], (uint32_t)(oc & 1), ab, a.status, 343));
         ++oc;
-      }
+        return done;
+      };
       // a single tile with a part in each accumulator: the groups exchange their
       // maxima and sums and share out the columns; else the group that has the
       // part writes all of it
       const bool share = pc.single && n1 > 0;
       float g0, g1, lt = l, mm = m_used;
       if (share) {
+        ok = o_done();
+        if (!ok) break;
         xmax[grp * BM + r] = m_used;
         xsum[grp * BM + r] = l;
         __syncwarp();
@@ -739,58 +744,72 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         g0 = grp == 0 ? 1.0f : 0.0f;
         g1 = 1.0f - g0;
       }
-      tc_fence_after();
+      // all that needs no output comes before the wait for the last product
       const float inv = lt > 0.0f ? 1.0f / lt : 0.0f;
       const float lse = lt > 0.0f ? (mm + __log2f(lt)) * 0.69314718055994531f : ninf;
       const bool mine = share || !pc.single || grp == 0;
       const int64_t orow = (int64_t)(pc.row0 + tok) * a.pd.H + (int64_t)pc.g * G + rh;
       const int64_t prow = (int64_t)pc.slot * a.slot_rows + (pc.single ? 0 : grp * BM) + r;
-      if (mine && active) {
-        const int c0 = share ? grp * (D / 64) : 0, c1 = share ? c0 + D / 64 : D / 32;
-        uint8_t* dst = pc.slot >= 0 ? reinterpret_cast<uint8_t*>(a.opart + prow * D)
-                                    : reinterpret_cast<uint8_t*>(a.O + orow * D);
+      uint8_t* dst = pc.slot >= 0 ? reinterpret_cast<uint8_t*>(a.opart + prow * D)
+                                  : reinterpret_cast<uint8_t*>(a.O + orow * D);
+      if (row_ok && (grp == 0 || !pc.single)) {
+        if (pc.slot >= 0)
+          a.lpart[prow] = lse;
+        else
+          a.lse[(int64_t)(pc.g * G + rh) * a.pd.T + pc.row0 + tok] = lse;
+      }
+      if (!share) {
+        ok = o_done();
+        if (!ok) break;
+      }
+      tc_fence_after();
+      // 32 columns of the row from c on
+      auto put = [&](int c, uint32_t* o) {
+        if (!row_ok) return;
+        if (pc.slot >= 0) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) store8(dst + c * 4 + e * 4, o + e, true);
+        } else {
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            w[e] = pack_bf16x2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+          store8(dst + c * 2, w, a.wide);
+          store8(dst + c * 2 + 32, w + 8, a.wide);
+        }
+      };
+      if (active && share) {
         g0 *= inv;
         g1 *= inv;
 #pragma unroll 1
-        for (int c = c0; c < c1; ++c) {
-          uint32_t o0[32];
-          if (share) {
-            uint32_t o1[32];
-            tmem_ld32(tl + C::TO + c * 32, o0);
-            tmem_ld32(tl + C::TO + C::TO_STEP + c * 32, o1);
-            tmem_wait_ld();
+        for (int c = grp * (D / 2); c < (grp + 1) * (D / 2); c += 32) {
+          uint32_t o0[32], o1[32];
+          tmem_ld32(tl + C::TO + c, o0);
+          tmem_ld32(tl + C::TO + C::TO_STEP + c, o1);
+          tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              o0[e] = __float_as_uint((g0 > 0.0f ? __uint_as_float(o0[e]) * g0 : 0.0f) +
-                                      (g1 > 0.0f ? __uint_as_float(o1[e]) * g1 : 0.0f));
-          } else if (pc.n > 0) {
-            tmem_ld32(tO + c * 32, o0);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              o0[e] = inv > 0.0f ? __float_as_uint(__uint_as_float(o0[e]) * inv) : 0u;
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o0[e] = 0u;
-          }
-          if (row_ok && pc.slot >= 0) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 8) store8(dst + c * 128 + e * 4, o0 + e, true);
-          } else if (row_ok) {
-            uint32_t w[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              w[e] = pack_bf16x2(__uint_as_float(o0[2 * e]), __uint_as_float(o0[2 * e + 1]));
-            store8(dst + c * 64, w, a.wide);
-            store8(dst + c * 64 + 32, w + 8, a.wide);
-          }
+          for (int e = 0; e < 32; ++e)
+            o0[e] = __float_as_uint((g0 > 0.0f ? __uint_as_float(o0[e]) * g0 : 0.0f) +
+                                    (g1 > 0.0f ? __uint_as_float(o1[e]) * g1 : 0.0f));
+          put(c, o0);
           __syncwarp();  // the loads from tensor memory are warp-wide
         }
-        if (row_ok && (grp == 0 || !pc.single)) {
-          if (pc.slot >= 0)
-            a.lpart[prow] = lse;
-          else
-            a.lse[(int64_t)(pc.g * G + rh) * a.pd.T + pc.row0 + tok] = lse;
+      } else if (active && mine) {
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          if (pc.n > 0) {
+            tmem_ld32(tO + c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              o[e] = inv > 0.0f ? __float_as_uint(__uint_as_float(o[e]) * inv) : 0u;
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0u;
+          }
+          put(c, o);
+          __syncwarp();
         }
       }
       if (share) {  // both groups have read both accumulators and the statistics
