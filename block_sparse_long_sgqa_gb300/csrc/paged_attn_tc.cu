@@ -79,26 +79,40 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Bounded wait of a whole warp that polls, with a warp-uniform outcome: for the
-// hand-offs of the product pipeline, where a suspended wait's wake-up costs more
-// than the polling.
-__device__ __forceinline__ bool warp_poll(uint64_t* bar, uint32_t parity, const Abort& ab,
-                                          int32_t* status, int where) {
-  if (__all_sync(FULL, mbar_test(bar, parity))) return true;
-  const uint64_t t0 = globaltimer();
-  for (uint32_t i = 1;; ++i) {
-    if (__all_sync(FULL, mbar_test(bar, parity))) return true;
-    if ((i & 255) == 0) {
-      int stop = 0;
-      if (ab.set()) {
-        stop = 1;
-      } else if (globaltimer() - t0 > kWaitLimitNs) {
-        if (lane_id() == 0) ab.raise(status, where);
-        stop = 1;
-      }
-      if (__any_sync(FULL, stop)) return false;
+// Once a role gives up waiting, the others stop at their next wait; the kernel's end
+// reports the detail.  (The waits are kept short: a tile's loop of all roles has to
+// stay in the instruction cache.)
+struct GiveUp {
+  volatile int* flag;
+  __device__ __forceinline__ bool now(uint64_t t0, int where, uint64_t limit_ns = kWaitLimitNs) const {
+    if (*flag != 0) return true;
+    if (globaltimer() - t0 <= limit_ns) return false;
+    *flag = where;
+    return true;
+  }
+};
+// Bounded wait of a warp, with a warp-uniform outcome.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const GiveUp& up, int where,
+                                          uint64_t limit_ns = kWaitLimitNs) {
+  bool there = mbar_try_wait(bar, parity);
+  if (!there) {
+    const uint64_t t0 = globaltimer();
+    for (uint32_t i = 1; !there; ++i) {
+      there = mbar_try_wait(bar, parity);
+      if ((i & 63) == 0 && !there && up.now(t0, where, limit_ns)) break;
     }
   }
+  return __all_sync(FULL, there);
+}
+// Same, polling: for the hand-offs of the product pipeline, where a suspended wait's
+// wake-up costs more than the polling.
+__device__ __forceinline__ bool warp_poll(uint64_t* bar, uint32_t parity, const GiveUp& up, int where) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 0; !__all_sync(FULL, mbar_test(bar, parity)); ++i) {
+    if (i == 0) t0 = globaltimer();
+    if ((i & 255) == 255 && __any_sync(FULL, up.now(t0, where))) return false;
+  }
+  return true;
 }
 
 // tcgen05.mma, bf16 operands and fp32 accumulation, from the low words of the
@@ -219,7 +233,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const Abort ab{abort_flag};
+  const GiveUp up{abort_flag};
   // The others sleep until the first piece is there: waiting on its barrier they
   // slowed the walk of warp 0 from 2 to 12 thousand cycles.
   if (warp != 0) asm volatile("bar.sync 1, 384;" ::: "memory");
@@ -279,35 +293,29 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       if (idle == 0) t_prog = globaltimer();
       __nanosleep(500);
       if ((++idle & 63) != 0) return true;
-      int stop = 0;
-      if (lane == 0) {
-        if (ab.set()) {
-          stop = 1;
-        } else if (globaltimer() - t_prog > kWaitLimitNs) {
-          ab.raise(a.status, 331);
-          stop = 1;
-        }
-      }
-      return !__shfl_sync(FULL, stop, 0);
+      return !__any_sync(FULL, up.now(t_prog, 331));
     };
     auto publish = [&](const Piece& pc) -> bool {
-      for (;;) {
-        if (pub - nq < NPC &&
+      for (bool there = false;;) {
+        if (!there && pub - nq < NPC &&
             __shfl_sync(FULL, (int)mbar_test(&pc_empty[pub % NPC], (uint32_t)(((pub / NPC) & 1) ^ 1)),
-                        0))
-          break;
-        if (!waited(pump())) return false;
+                        0)) {
+          if (lane == 0) {
+            piece_at(pub) = pc;
+            mbar_arrive(&pc_full[pub % NPC]);
+          }
+          __syncwarp();
+          if (pub == 0) asm volatile("bar.arrive 1, 384;" ::: "memory");
+          ++pub;
+          there = true;
+        }
+        const bool moved = pump();
+        if (there) {
+          idle = 0;
+          return true;
+        }
+        if (!waited(moved)) return false;
       }
-      idle = 0;
-      if (lane == 0) {
-        piece_at(pub) = pc;
-        mbar_arrive(&pc_full[pub % NPC]);
-      }
-      __syncwarp();
-      if (pub == 0) asm volatile("bar.arrive 1, 384;" ::: "memory");
-      ++pub;
-      pump();
-      return true;
     };
 
     int4 rec;
@@ -319,7 +327,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       ok = publish(pc);
     }
     while (ok && nq < pub) ok = waited(pump());
-    if (lane == 0 && ab.set())
+    if (lane == 0 && *up.flag != 0)
       for (int i = 0; i < 2; ++i)
         if (loaded >> i & 1u) mbar_wait_drain(&q_full[i], (lph >> i) & 1u, a.status, 391);
   } else if (warp <= 2) {
@@ -335,7 +343,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     int cnt = 0;  // tiles loaded
     bool ok = true;
     for (int i = 0; ok; ++i) {
-      ok = __all_sync(FULL, mbar_wait(&pc_full[i % NPC], (uint32_t)((i / NPC) & 1), ab, a.status, 332));
+      ok = warp_wait(&pc_full[i % NPC], (uint32_t)((i / NPC) & 1), up, 332);
       if (!ok) break;
       const Piece pc = piece_at(i);
       __syncwarp();
@@ -356,8 +364,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
         const int boxes = __popc(__ballot_sync(FULL, on));
         const int sl = cnt % NS;
-        ok = __all_sync(FULL, mbar_wait(&empty[sl], (uint32_t)(((cnt / NS) & 1) ^ 1), ab, a.status,
-                                        isK ? 333 : 334));
+        ok = warp_wait(&empty[sl], (uint32_t)(((cnt / NS) & 1) ^ 1), up, isK ? 333 : 334);
         if (!ok) break;
         if (lane == 0) mbar_expect_tx(&full[sl], (uint32_t)(boxes * a.box * 128 * C::KC));
         __syncwarp();
@@ -368,7 +375,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         __syncwarp();
       }
     }
-    if (lane == 0 && ab.set())  // copies in flight land before the CTA ends
+    if (lane == 0 && *up.flag != 0)  // copies in flight land before the CTA ends
       for (int k = 0; k < NS; ++k) {
         const int uses = cnt / NS + (k < cnt % NS ? 1 : 0);
         if (uses > 0) mbar_wait_drain(&full[k], (uint32_t)((uses - 1) & 1), a.status, isK ? 392 : 393);
@@ -398,20 +405,20 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     uint32_t qph = 0;               // phases of q_full, bit = slot
     bool first = true, ok = true;
     for (int i = 0; ok; ++i) {
-      ok = warp_poll(&pc_full[i % NPC], (uint32_t)((i / NPC) & 1), ab, a.status, 335);
+      ok = warp_poll(&pc_full[i % NPC], (uint32_t)((i / NPC) & 1), up, 335);
       if (!ok) break;
       const Piece& pc = piece_at(i);
       // (reductions of equal values: uniform registers)
       const int n = __reduce_max_sync(FULL, pc.n), single = __reduce_max_sync(FULL, pc.single);
       const int end = __reduce_max_sync(FULL, pc.end);
       if (n > 0) {
-        ok = warp_poll(&q_full[single ? qs : 0], (qph >> (single ? qs : 0)) & 1u, ab, a.status, 336) &&
-             (single || warp_poll(&q_full[1], qph >> 1, ab, a.status, 336));
+        ok = warp_poll(&q_full[single ? qs : 0], (qph >> (single ? qs : 0)) & 1u, up, 336) &&
+             (single || warp_poll(&q_full[1], qph >> 1, up, 336));
         // Debug request (host-set status[3]): the first piece waits on a barrier
         // nothing arrives on, so the pipeline gives up (detail 220) while its K
         // and V copies are in flight.
         if (ok && first && blockIdx.x == 0 && debug_request(a.status) == SGQA_DEBUG_STALL)
-          ok = __all_sync(FULL, mbar_wait(stall_bar, 0, ab, a.status, 220, kDebugStallNs));
+          ok = warp_wait(stall_bar, 0, up, 220, kDebugStallNs);
         if (!ok) break;
         qph ^= single ? 1u << qs : 3u;
         first = false;
@@ -494,18 +501,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             idle = 0;
           } else {
             if (idle == 0) t_prog = globaltimer();
-            if ((++idle & 255) == 0) {
-              int stop = 0;
-              if (ab.set()) {
-                stop = 1;
-              } else if (globaltimer() - t_prog > kWaitLimitNs) {
-                if (lane == 0) ab.raise(a.status, 337);
-                stop = 1;
-              }
-              if (__any_sync(FULL, stop)) {
-                ok = false;
-                break;
-              }
+            if ((++idle & 255) == 0 && __any_sync(FULL, up.now(t_prog, 337))) {
+              ok = false;
+              break;
             }
           }
         }
@@ -514,7 +512,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         // of one thread run in issue order.  The next key tile is looked for while P
         // is waited for, so that the two are issued without a pause.
         auto k_there = [&](int j) -> bool {
-          return (j & sh) != 0 || warp_poll(&k_full[ks], kph, ab, a.status, 337);
+          return (j & sh) != 0 || warp_poll(&k_full[ks], kph, up, 337);
         };
         for (int j = 0; ok && j < 2 && j < J; ++j) {
           ok = k_there(j);
@@ -532,14 +530,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             if (__all_sync(FULL, there)) break;
             if ((i2 & 255) == 255) {
               if (t_prog == 0) t_prog = globaltimer();
-              int stop = 0;
-              if (ab.set()) {
-                stop = 1;
-              } else if (globaltimer() - t_prog > kWaitLimitNs) {
-                if (lane == 0) ab.raise(a.status, 339);
-                stop = 1;
-              }
-              if (__any_sync(FULL, stop)) {
+              if (__any_sync(FULL, up.now(t_prog, 339))) {
                 ok = false;
                 break;
               }
@@ -577,7 +568,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     int sc = 0, oc = 0, xc = 0, vbase = 0;
     bool ok = true;
     for (int i = 0; ok; ++i) {
-      ok = __all_sync(FULL, mbar_wait(&pc_full[i % NPC], (uint32_t)((i / NPC) & 1), ab, a.status, 340));
+      ok = warp_wait(&pc_full[i % NPC], (uint32_t)((i / NPC) & 1), up, 340);
       if (!ok) break;
       const Piece pc = piece_at(i);
       __syncwarp();
@@ -594,7 +585,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       const int t0 = pc.single ? grp : 0;
       for (int t = t0; t < pc.n; t += step) {
         const int k0 = (pc.tb + t) * KB;
-        ok = __all_sync(FULL, mbar_wait(&s_full[grp], (uint32_t)(sc & 1), ab, a.status, 341));
+        ok = warp_wait(&s_full[grp], (uint32_t)(sc & 1), up, 341);
         if (!ok) break;
         ++sc;
         tc_fence_after();
@@ -603,7 +594,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         auto p_free = [&]() -> bool {
           if constexpr (C::OWN_P) {
             if (sc > 1)
-              return __all_sync(FULL, mbar_wait(&p_empty[grp], (uint32_t)(sc & 1), ab, a.status, 348));
+              return warp_wait(&p_empty[grp], (uint32_t)(sc & 1), up, 348);
           }
           return true;
         };
@@ -693,7 +684,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         // S is there: only then has the slot's last tile been used.)
         if ((pc.single || grp == 0) && (pc.lo > k0 || pc.hi < k0 + KB)) {
           const int vt = vbase + t, vs = vt % C::SV;
-          ok = __all_sync(FULL, mbar_wait(&v_full[vs], (uint32_t)((vt / C::SV) & 1), ab, a.status, 342));
+          ok = warp_wait(&v_full[vs], (uint32_t)((vt / C::SV) & 1), up, 342);
           if (!ok) break;
           if (k0 + r < pc.lo || k0 + r >= pc.hi) {
             uint8_t* vr = smem + C::OFF_V + vs * C::TILE + r * 128;
@@ -717,7 +708,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       auto o_done = [&]() -> bool {
         if ((grp == 0 ? n0 : n1) == 0) return true;
         const bool done =
-            __all_sync(FULL, mbar_wait(&o_full[grp], (uint32_t)(oc & 1), ab, a.status, 343));
+            warp_wait(&o_full[grp], (uint32_t)(oc & 1), up, 343);
         ++oc;
         return done;
       };
@@ -733,7 +724,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         xsum[grp * BM + r] = l;
         __syncwarp();
         if (lane == 0) mbar_arrive(&x_bar[0]);
-        ok = __all_sync(FULL, mbar_wait(&x_bar[0], (uint32_t)(xc & 1), ab, a.status, 345));
+        ok = warp_wait(&x_bar[0], (uint32_t)(xc & 1), up, 345);
         if (!ok) break;
         const float m0 = xmax[r], m1 = xmax[BM + r];
         mm = fmaxf(m0, m1);
@@ -816,13 +807,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&x_bar[1]);
-        ok = __all_sync(FULL, mbar_wait(&x_bar[1], (uint32_t)(xc & 1), ab, a.status, 346));
+        ok = warp_wait(&x_bar[1], (uint32_t)(xc & 1), up, 346);
         ++xc;
       }
     }
     tc_fence_before();
   }
   __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag != 0) report(a.status, SGQA_ERR_TIMEOUT, *abort_flag);
   if (warp == 3) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
