@@ -22,8 +22,8 @@
 // heads in 600 us, 7.2 TB/s; 64 ragged contexts in 363 us, 6.8 TB/s).  Chunks: the
 // chain of a group from S to P to the products that give the next S, 2970 cycles for
 // the 2 x 1050 that the products of both groups take (4096 tokens over 36K keys, 64
-// heads: 3.05 ms, 1530 TFLOP/s; the tensor pipe is 66 % active).  Short pieces (a
-// window of 512 keys, 169 us): 5 of a piece's 21 thousand cycles pass between the last
+// heads: 3.05 to 3.1 ms, 1510 TFLOP/s; the tensor pipe is 66 % active).  Short pieces (a
+// window of 512 keys, 167 us): 5 of a piece's 21 thousand cycles pass between the last
 // P and the next first S, and three of its five key tiles are masked.
 #include "paged_line.cuh"
 
@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         return true;
       }
       if (idle == 0) t_prog = globaltimer();
-      __nanosleep(500);
+      __nanosleep(1000);  // (500: windowed chunks 1 % slower)
       if ((++idle & 63) != 0) return true;
       return !__any_sync(FULL, up.now(t_prog, 331));
     };
@@ -472,12 +472,23 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
       };
       if constexpr (C::OWN_P) {
-        // Both products as soon as what they need is there, each kind in step order
+        // Both products as soon as what they need is there, each kind in step order; P
+        // first (4096 tokens over 32768 keys, 32 heads: 1280 us, S first 1309).  A warp
+        // for each kind, with one for both loads, was slower (window 201 us).
         int nqk = 0, npv = 0;
         uint64_t t_prog = 0;
         uint32_t idle = 0;
         while (npv < J) {
           bool progress = false;
+          if (npv < nqk) {
+            const int g = npv & 1;
+            if (__all_sync(FULL, mbar_test(&p_full[g], (pph >> g) & 1u) &&
+                                     ((npv & sh) != 0 || mbar_test(&v_full[vs], vph)))) {
+              pph ^= 1u << g;
+              pv(npv++);
+              progress = true;
+            }
+          }
           if (nqk < J) {
             const int g = nqk & 1;
             if (__all_sync(FULL, ((used >> g & 1u) == 0u || mbar_test(&s_empty[g], (sph >> g) & 1u)) &&
@@ -485,15 +496,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
               if (used >> g & 1u) sph ^= 1u << g;
               used |= 1u << g;
               qk(nqk++);
-              progress = true;
-            }
-          }
-          if (npv < nqk) {
-            const int g = npv & 1;
-            if (__all_sync(FULL, mbar_test(&p_full[g], (pph >> g) & 1u) &&
-                                     ((npv & sh) != 0 || mbar_test(&v_full[vs], vph)))) {
-              pph ^= 1u << g;
-              pv(npv++);
               progress = true;
             }
           }
@@ -754,42 +756,23 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (!ok) break;
       }
       tc_fence_after();
-      // 32 columns of the row from c on
-      auto put = [&](int c, uint32_t* o) {
-        if (!row_ok) return;
-        if (pc.slot >= 0) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 8) store8(dst + c * 4 + e * 4, o + e, true);
-        } else {
-          uint32_t w[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            w[e] = pack_bf16x2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
-          store8(dst + c * 2, w, a.wide);
-          store8(dst + c * 2 + 32, w + 8, a.wide);
-        }
-      };
-      if (active && share) {
+      if (active && mine) {
         g0 *= inv;
         g1 *= inv;
+        const int c0 = share ? grp * (D / 2) : 0, c1 = share ? c0 + D / 2 : D;
 #pragma unroll 1
-        for (int c = grp * (D / 2); c < (grp + 1) * (D / 2); c += 32) {
-          uint32_t o0[32], o1[32];
-          tmem_ld32(tl + C::TO + c, o0);
-          tmem_ld32(tl + C::TO + C::TO_STEP + c, o1);
-          tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            o0[e] = __float_as_uint((g0 > 0.0f ? __uint_as_float(o0[e]) * g0 : 0.0f) +
-                                    (g1 > 0.0f ? __uint_as_float(o1[e]) * g1 : 0.0f));
-          put(c, o0);
-          __syncwarp();  // the loads from tensor memory are warp-wide
-        }
-      } else if (active && mine) {
-#pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
+        for (int c = c0; c < c1; c += 32) {
           uint32_t o[32];
-          if (pc.n > 0) {
+          if (share) {
+            uint32_t o1[32];
+            tmem_ld32(tl + C::TO + c, o);
+            tmem_ld32(tl + C::TO + C::TO_STEP + c, o1);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              o[e] = __float_as_uint((g0 > 0.0f ? __uint_as_float(o[e]) * g0 : 0.0f) +
+                                     (g1 > 0.0f ? __uint_as_float(o1[e]) * g1 : 0.0f));
+          } else if (pc.n > 0) {
             tmem_ld32(tO + c, o);
             tmem_wait_ld();
 #pragma unroll
@@ -799,8 +782,18 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = 0u;
           }
-          put(c, o);
-          __syncwarp();
+          if (row_ok && pc.slot >= 0) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) store8(dst + c * 4 + e * 4, o + e, true);
+          } else if (row_ok) {
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              w[e] = pack_bf16x2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+            store8(dst + c * 2, w, a.wide);
+            store8(dst + c * 2 + 32, w + 8, a.wide);
+          }
+          __syncwarp();  // the loads from tensor memory are warp-wide
         }
       }
       if (share) {  // both groups have read both accumulators and the statistics
