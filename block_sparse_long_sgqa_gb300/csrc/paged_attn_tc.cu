@@ -867,8 +867,8 @@ int launch_paged_tc(const PagedDims& pd, const PagedAttnArgs& pa, void* ws, cuda
   a.tpm = BM / pd.G;
   a.tiles_per_item = 2;
   a.tile_rows = BM;
-  // 0.8 us a tile: four contexts of 300 to 2047 keys 16.8 us, one of 8K 22.3 (8 and 4:
-  // 17.4 and 24.0; 8 and 8: 17.2 and 21.9; cut evenly over all CTAs: 20.0 and 27.4)
+  // 0.8 us a tile: four contexts of 300 to 2047 keys 15.6 us, one of 8K 22 (about 1 us
+  // more with 8 and 4 or 8 and 8, 4 us more cut evenly over all CTAs)
   a.whole = 8;
   a.part = 6;
   a.uncut = pd.cap <= a.whole * KB;
