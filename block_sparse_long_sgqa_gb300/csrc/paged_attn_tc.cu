@@ -867,6 +867,7 @@ int launch_paged_tc(const PagedDims& pd, const PagedAttnArgs& pa, void* ws, cuda
   a.tpm = BM / pd.G;
   a.tiles_per_item = 2;
   a.tile_rows = BM;
+  a.over = 3;  // (2: mixed chunk 106.8 us for 104.8; 4: 105.7)
   // 0.8 us a tile: four contexts of 300 to 2047 keys 15.6 us, one of 8K 22 (about 1 us
   // more with 8 and 4 or 8 and 8, 4 us more cut evenly over all CTAs)
   a.whole = 8;

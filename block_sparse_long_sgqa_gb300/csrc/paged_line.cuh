@@ -31,6 +31,7 @@ struct LineArgs {
   int heads;             // query heads of a group (the last of a KV head: at most)
   int tpm;               // tokens of a query tile
   int tiles_per_item;    // query tiles of an item of longer requests: 1 or 2
+  int over;              // key tiles that an item's beginning and end count for, >= 1 (a window: 2)
   int whole, part;       // key tiles of an uncut item and of a part, in small calls
   int uncut;             // no item is longer than `whole`: none is ever cut, nothing to merge
   int tile_rows;         // rows from one query tile of a partial output to the next
@@ -52,11 +53,10 @@ struct Piece {
 };
 
 // Lengths on the line, in keys times a weight: a key tile takes kWt[..] * KB
-// (two query tiles cost about half as much again as one), an item kOver tiles
-// more for its beginning and end.  kOver >= 2 also keeps every tile's place
-// inside its item (an item's first and last tile may reach past its keys).
+// (two query tiles cost about half as much again as one), an item `over` tiles
+// more for its beginning and end.  That also keeps every tile's place inside its
+// item: the last tile may reach past the item's keys and, with a window, the first.
 constexpr int kWtSingle = 2, kWtDouble = 3;
-constexpr int kOver = 3;
 // Shortest range of a CTA, in key tiles of a single query tile.
 constexpr int kLeastTiles = 2;
 // A range that ends within kSnap tiles of an item's beginning or end leaves the
@@ -105,7 +105,7 @@ __device__ __forceinline__ Cut cut_of(const LineArgs& a, int s, bool tell) {
   }
   // (a window's first key may lie anywhere in its tile)
   c.tiles = a.pd.window > 0 ? min((keys + KB - 1) / KB + 1, (q.kv + KB - 1) / KB) : (q.kv + KB - 1) / KB;
-  c.A = (int64_t)(keys + kOver * KB) * wt;
+  c.A = (int64_t)(keys + a.over * KB) * wt;
   c.B = (int64_t)slope * wt;
   c.head = c.A * c.items + c.B * ((int64_t)c.items * (c.items - 1) / 2);
   return c;
