@@ -228,8 +228,8 @@ __device__ __noinline__ void simt_piece(const SimtArgs& a, const Piece pc, float
     const int tok = r / a.heads, h = r - tok * a.heads;
     if (r >= rows || h >= nh) continue;
     const int64_t t = pc.row0 + tok, hq = h0 + h;
-    const float inv = lt > 0.f ? 1.f / lt : 0.f;
-    const float lse = lt > 0.f ? (m[i] + log2f(lt)) * 0.69314718055994531f : ninf;
+    const float inv = lt != 0.f ? 1.f / lt : 0.f;
+    const float lse = lt != 0.f ? (m[i] + log2f(lt)) * 0.69314718055994531f : ninf;
     const int64_t part = (int64_t)pc.slot * a.slot_rows + r;
     float* dst = pc.slot >= 0 ? a.opart + part * D : a.O + (t * a.pd.H + hq) * D;
 #pragma unroll
@@ -479,12 +479,12 @@ __device__ __noinline__ void few_piece(const SimtArgs& a, const Piece pc, float*
       acc.w = fmaf(f, v.w, acc.w);
     }
     const int64_t t = pc.row0 + tok, hq = h0 + h;
-    const float inv = lt > 0.f ? 1.f / lt : 0.f;
+    const float inv = lt != 0.f ? 1.f / lt : 0.f;
     const int64_t slot_row = (int64_t)pc.slot * a.slot_rows + r;
     float* dst = pc.slot >= 0 ? a.opart + slot_row * D : a.O + (t * a.pd.H + hq) * D;
     *reinterpret_cast<float4*>(dst + c0) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
     if (c0 == 0) {
-      const float lse = lt > 0.f ? (mm + log2f(lt)) * 0.69314718055994531f : ninf;
+      const float lse = lt != 0.f ? (mm + log2f(lt)) * 0.69314718055994531f : ninf;
       (pc.slot >= 0 ? a.lpart[slot_row] : a.lse[hq * a.pd.T + t]) = lse;
     }
   }

@@ -19,7 +19,7 @@
 // run on across pieces, so the next piece's keys load during the current one.
 //
 // What bounds it.  Single tokens over long caches: the bytes of K and V (1M keys of 8
-// heads in 600 us, 7.2 TB/s; 64 ragged contexts in 363 us, 6.8 TB/s).  Chunks: the
+// heads in 590 us, 7.3 TB/s; 64 ragged contexts in 356 us, 6.9 TB/s).  Chunks: the
 // chain of a group from S to P to the products that give the next S, 2970 cycles for
 // the 2 x 1050 that the products of both groups take (4096 tokens over 36K keys, 64
 // heads: 3.05 to 3.1 ms, 1510 TFLOP/s; the tensor pipe is 66 % active).  Short pieces (a
@@ -738,8 +738,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         g1 = 1.0f - g0;
       }
       // all that needs no output comes before the wait for the last product
-      const float inv = lt > 0.0f ? 1.0f / lt : 0.0f;
-      const float lse = lt > 0.0f ? (mm + __log2f(lt)) * 0.69314718055994531f : ninf;
+      const float inv = lt != 0.0f ? 1.0f / lt : 0.0f;  // (a NaN stays one)
+      const float lse = lt != 0.0f ? (mm + __log2f(lt)) * 0.69314718055994531f : ninf;
       const bool mine = share || !pc.single || grp == 0;
       const int64_t orow = (int64_t)(pc.row0 + tok) * a.pd.H + (int64_t)pc.g * G + rh;
       const int64_t prow = (int64_t)pc.slot * a.slot_rows + (pc.single ? 0 : grp * BM) + r;
@@ -770,14 +770,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              o[e] = __float_as_uint((g0 > 0.0f ? __uint_as_float(o[e]) * g0 : 0.0f) +
-                                     (g1 > 0.0f ? __uint_as_float(o1[e]) * g1 : 0.0f));
+              o[e] = __float_as_uint((g0 != 0.0f ? __uint_as_float(o[e]) * g0 : 0.0f) +
+                                     (g1 != 0.0f ? __uint_as_float(o1[e]) * g1 : 0.0f));
           } else if (pc.n > 0) {
             tmem_ld32(tO + c, o);
             tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              o[e] = inv > 0.0f ? __float_as_uint(__uint_as_float(o[e]) * inv) : 0u;
+              o[e] = lt != 0.0f ? __float_as_uint(__uint_as_float(o[e]) * inv) : 0u;
           } else {
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = 0u;
@@ -868,11 +868,11 @@ int launch_paged_tc(const PagedDims& pd, const PagedAttnArgs& pa, void* ws, cuda
   a.tiles_per_item = 2;
   a.tile_rows = BM;
   a.over = 3;  // (2: mixed chunk 106.8 us for 104.8; 4: 105.7)
-  // 0.8 us a tile: four contexts of 300 to 2047 keys 15.6 us, one of 8K 22 (about 1 us
-  // more with 8 and 4 or 8 and 8, 4 us more cut evenly over all CTAs)
-  a.whole = 8;
-  a.part = 6;
-  a.uncut = pd.cap <= a.whole * KB;
+  // 0.8 us a tile, 4 us for a merge: four contexts of 300 to 2047 keys 14.1 us, of 1000
+  // to 5000 16.3 (8 and 6: 14.7 and 18.0; 4 and 3: 15.2 and 17.2).  Without a merge when
+  // no cache is longer than 8 tiles: 1000 keys 12.5 us, against 12.9.
+  a.whole = a.part = 4;
+  a.uncut = pd.cap <= 8 * KB;
   a.O = static_cast<__nv_bfloat16*>(pa.O);
   a.lse = pa.lse;
   int x = pd.ps, y = KB;

@@ -490,6 +490,29 @@ def test_attention_peaked(s, name, dtype):
 
 @gpu
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("name", ["decode", "decode_split_16", "few_g16", "chunk", "mixed_idle"])
+def test_attention_nan_stays_with_its_rows(s, name, dtype):
+    """A NaN key makes the rows that see it NaN, in O and lse, whole or cut items
+    alike; other requests and other heads keep their bits."""
+    b, p, wide, K, V, q_start, kw = attn_case(s, name, dtype)
+    O, lse, code = run_attn(s, p, wide, K, V, b.table, q_start, b.kv)
+    assert code == s.OK
+    i = int(np.argmax(b.kv * (b.q > 0)))
+    pos, g, G = int(b.kv[i] - b.q[i]) // 2, p.n_kv_heads - 1, p.n_q_heads // p.n_kv_heads
+    K[b.table[i, pos // b.ps], g, pos % b.ps, 5] = float("nan")
+    On, ln, code = run_attn(s, p, wide, K, V, b.table, q_start, b.kv)
+    assert code == s.OK
+    rows = torch.zeros(p.max_tokens, dtype=torch.bool)
+    rows[q_start[i]:q_start[i + 1]] = True
+    heads = torch.zeros(p.n_q_heads, dtype=torch.bool)
+    heads[g * G:(g + 1) * G] = True
+    hit = (rows[:, None] & heads[None, :]).cuda()
+    assert torch.isnan(On[hit]).all() and torch.isnan(ln.T[hit]).all()
+    assert torch.equal(On[~hit], O[~hit]) and torch.equal(ln.T[~hit], lse.T[~hit])
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_attention_repeats_bit_for_bit(s, dtype):
     for name in ("decode_long", "mixed_idle", "chunk"):
         b, p, wide, K, V, q_start, kw = attn_case(s, name, dtype)
