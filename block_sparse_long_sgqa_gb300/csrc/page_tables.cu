@@ -134,11 +134,10 @@ __device__ void totals(Shared& sh, int N, F one, uint64_t& tok, uint64_t& pages)
 }
 
 __global__ void __launch_bounds__(NT)
-    k_page_plan(PagedDims pd, const int32_t* __restrict__ q_len,
-                const int32_t* __restrict__ kv_len, const int32_t* __restrict__ free_pages,
-                const int32_t* __restrict__ n_free_p, int32_t* page_table, int32_t* q_start,
-                int64_t* __restrict__ slot_map, int32_t* __restrict__ positions,
-                int32_t* n_free_out, int32_t* status) {
+    k_page_plan(PagedDims pd, const int32_t* q_len, const int32_t* kv_len,
+                const int32_t* free_pages, const int32_t* n_free_p, int32_t* page_table,
+                int32_t* q_start, int64_t* slot_map, int32_t* positions, int32_t* n_free_out,
+                int32_t* status) {
   __shared__ Shared sh;
   pdl_next();
   pdl_wait();
@@ -234,9 +233,8 @@ __global__ void __launch_bounds__(NT)
 // Pages of the requests' tails pushed on the stack: the same sums, over the
 // pages given back; CTAs serve equal ranges of them.
 __global__ void __launch_bounds__(NT)
-    k_page_release(PagedDims pd, const int32_t* __restrict__ kv_len,
-                   const int32_t* __restrict__ keep_len, const int32_t* __restrict__ page_table,
-                   int32_t* free_pages, const int32_t* __restrict__ n_free_p,
+    k_page_release(PagedDims pd, const int32_t* kv_len, const int32_t* keep_len,
+                   const int32_t* page_table, int32_t* free_pages, const int32_t* n_free_p,
                    int32_t* n_free_out, int32_t* status) {
   __shared__ Shared sh;
   pdl_next();

@@ -51,7 +51,10 @@ int launch_paged_tc(const PagedDims& pd, const PagedAttnArgs& a, void* ws, cudaS
 // Launches in a row: each kernel lets the next one be scheduled from its start on
 // (pdl_next) and, before it touches memory that another kernel may still read or write,
 // waits until the one before it is complete (pdl_wait).  The next launch's latency and
-// set-up then lie beside the end of this one's work.
+// set-up then lie beside the end of this one's work.  No pointer of such a kernel is
+// __restrict__: what it points to may be written until the wait returns, and the
+// qualifier would allow loads through the non-coherent path, or ahead of the wait,
+// whose memory clobber need not order them.
 __device__ __forceinline__ void pdl_next() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }

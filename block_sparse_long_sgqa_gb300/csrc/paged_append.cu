@@ -7,11 +7,12 @@ namespace sgqa {
 namespace {
 
 // One warp per token: its K row and its V row, Hkv * d values each, move as
-// 16-byte units (up[] of them per head, a power of two).
+// 16-byte units (2^log_up of them per head), kBatch of each row a lane at a time
+// with their loads before their stores.
+constexpr int kBatch = 4;
 __global__ void __launch_bounds__(256)
-    k_paged_append(PagedDims pd, const uint4* __restrict__ K, const uint4* __restrict__ V,
-                   const int64_t* __restrict__ slot_map, uint4* __restrict__ Kp,
-                   uint4* __restrict__ Vp, int log_up, int64_t row_units, int32_t* status) {
+    k_paged_append(PagedDims pd, const uint4* K, const uint4* V, const int64_t* slot_map,
+                   uint4* Kp, uint4* Vp, int log_up, int64_t row_units, int32_t* status) {
   pdl_next();
   pdl_wait();
   const int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -28,12 +29,24 @@ __global__ void __launch_bounds__(256)
   const uint4* k = K + t * row_units;
   const uint4* v = V + t * row_units;
   const int64_t base = (int64_t)page * pd.Hkv * pd.ps + off;  // row of head 0
-  for (int u = lane; u < units; u += 32) {
-    const int g = u >> log_up, c = u & ((1 << log_up) - 1);
-    const int64_t at = ((base + (int64_t)g * pd.ps) << log_up) + c;
-    const uint4 x = k[u], y = v[u];
-    Kp[at] = x;
-    Vp[at] = y;
+  for (int u0 = lane; u0 < units; u0 += 32 * kBatch) {
+    uint4 x[kBatch], y[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int u = u0 + 32 * b;
+      if (u >= units) break;
+      x[b] = k[u];
+      y[b] = v[u];
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int u = u0 + 32 * b;
+      if (u >= units) break;
+      const int g = u >> log_up, c = u & ((1 << log_up) - 1);
+      const int64_t at = ((base + (int64_t)g * pd.ps) << log_up) + c;
+      Kp[at] = x[b];
+      Vp[at] = y[b];
+    }
   }
 }
 

@@ -384,8 +384,8 @@ __device__ __forceinline__ bool walk_line(const LineArgs& a, Cut cut, const Line
 // thread; one context of 8K: 6 against 9.  Eight parts together: 2 us more on the mixed
 // requests (registers leave half the warps).
 template <typename E, int D, int GRID, int NT>
-__global__ void __launch_bounds__(NT) k_paged_merge(const __grid_constant__ LineArgs a,
-                                                    E* __restrict__ O, float* __restrict__ lse) {
+__global__ void __launch_bounds__(NT) k_paged_merge(const __grid_constant__ LineArgs a, E* O,
+                                                    float* lse) {
   static_assert(GRID <= NT, "a thread per CTA of the attention");
   __shared__ int4 rec[GRID];
   __shared__ int ends[GRID];  // rows of the items up to and with c

@@ -1,0 +1,116 @@
+"""Paged serving operators at their edges: calls in a row with nothing between
+them, values and tables that the operators promise to leave alone, refusals."""
+import os
+import re
+
+import numpy as np
+import pytest
+import torch
+
+import paged_ref as ref
+from test_paged import Batch, attn_case, check_attn, dev, params, run_attn, status_of
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "block_sparse_long_sgqa_gb300", "csrc")
+gpu = pytest.mark.gpu
+both = pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+
+
+@pytest.fixture(scope="module")
+def s():
+    from block_sparse_long_sgqa_gb300 import sgqa
+
+    return sgqa
+
+
+# ----------------------------------------------------------- calls in a row
+def test_no_restrict_behind_a_dependent_launch():
+    """A kernel that may start while the one before it still writes its inputs
+    declares none of its pointers __restrict__."""
+    seen = 0
+    for name in os.listdir(CSRC):
+        text = open(os.path.join(CSRC, name)).read()
+        if not name.startswith("pa"):
+            assert "launch_pdl" not in text, name
+            continue
+        for m in re.finditer(r"__global__[^{;]*", text):
+            if "pdl_wait" in text[m.end():m.end() + 20000]:
+                seen += 1
+                assert "__restrict__" not in m.group(0), (name, m.group(0))
+    assert seen >= 4
+
+
+@gpu
+@both
+def test_captured_chain_of_steps(s, dtype):
+    """Several steps in one graph, each plan -> append -> attention -> release with
+    nothing between the launches and the free counts in two buffers that take
+    turns: every table, slot, count and output as in the step-by-step form."""
+    rng = np.random.default_rng(21)
+    g = torch.Generator().manual_seed(22)
+    N, H, hk, d, ps, steps = 40, 4, 2, 64, 8, 5
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    kv0 = rng.integers(0, 60, N)
+    lens, cur = [], kv0
+    for k in range(steps):
+        q = np.where(rng.random(N) < 0.2, 0, rng.integers(0, 10, N))
+        kv = cur + q
+        cur = kv0 if k == steps - 1 else rng.integers(kv0, kv + 1)
+        lens.append((q, kv, cur))  # the last release leaves the lengths of the start
+    T = max(int(q.sum()) for q, _, _ in lens) + 3
+    b = Batch(23, [0] * N, kv0, ps, spare=200, extra_cols=10, held_at="after")
+    p = params(s, n_seqs=N, max_tokens=T, n_q_heads=H, n_kv_heads=hk, head_dim=d, page_size=ps,
+               n_pages=b.n_pages, max_pages=b.max_pages,
+               dtype=s.BF16 if dtype == "bf16" else s.FP32)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    free, table = dev(b.free), dev(b.table)
+    nf, nf2 = torch.full((1,), b.n_free, **i32), torch.full((1,), -1, **i32)
+    Kp, Vp = (torch.randn(b.n_pages, hk, ps, d, generator=g).to(dt) for _ in "kv")
+    pool = [Kp.double().numpy(), Vp.double().numpy()]  # the host's copy
+    Kp, Vp = Kp.cuda(), Vp.cuda()
+    ws, st = s.alloc_paged_workspace(p), s.new_status()
+    io = []
+    for q, kv, keep in lens:
+        x = torch.randn(T, H + 2 * hk, d, generator=g).to(dt)
+        io.append(dict(
+            q=dev(q).int(), kv=dev(kv).int(), keep=dev(keep).int(), host=x.double().numpy(),
+            Q=x[:, :H].contiguous().cuda(), K=x[:, H:H + hk].contiguous().cuda(),
+            V=x[:, H + hk:].contiguous().cuda(), q_start=torch.zeros(N + 1, **i32),
+            slots=torch.zeros(T, dtype=torch.int64, device="cuda"), pos=torch.zeros(T, **i32),
+            O=torch.zeros(T, H, d, dtype=dt, device="cuda"), lse=torch.zeros(H, T, device="cuda")))
+
+    def chain():
+        for v in io:
+            s.sgqa_page_plan(p, v["q"], v["kv"], free, nf, table, v["q_start"], v["slots"],
+                             v["pos"], nf2, status=st)
+            s.sgqa_paged_append(p, v["K"], v["V"], v["slots"], Kp, Vp, status=st)
+            s.sgqa_paged_attn(p, v["Q"], Kp, Vp, table, v["q_start"], v["kv"], v["O"], v["lse"],
+                              ws, status=st)
+            s.sgqa_page_release(p, v["kv"], v["keep"], table, free, nf2, nf, status=st)
+
+    cg = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(cg):
+        chain()
+    h_table, h_free, h_n = b.table, b.free, b.n_free
+    for it in range(4):  # three replays, then the same calls without a graph
+        (cg.replay if it < 3 else chain)()
+        assert status_of(s, st) == s.OK
+        for v, (q, kv, keep) in zip(io, lens):
+            h_table, q_start, slots, pos, h_n = ref.plan(q, kv, h_free, h_n, h_table, ps, T)
+            assert np.array_equal(v["q_start"].cpu().numpy(), q_start)
+            assert np.array_equal(v["slots"].cpu().numpy(), slots)
+            assert np.array_equal(v["pos"].cpu().numpy(), pos)
+            n = int(q_start[-1])
+            for i, c0 in enumerate((H, H + hk)):
+                pool[i][slots[:n] // ps, :, slots[:n] % ps] = v["host"][:n, c0:c0 + hk]
+            R, z, tO, tl, mine = ref.attention(v["host"][:, :H], *pool, ps, h_table, q_start, kv,
+                                               ref.default_scale(d), True, 0, dtype == "bf16")
+            assert (np.abs(v["O"].double().cpu().numpy() - R)[mine] <= tO[mine]).all()
+            assert (np.abs(v["lse"].double().cpu().numpy() - z)[:, mine] <= tl[:, mine]).all()
+            h_free, h_n = ref.release(kv, keep, h_table, h_free, h_n, ps)
+        assert nf.item() == h_n
+        assert np.array_equal(free.cpu().numpy(), h_free)
+        assert np.array_equal(table.cpu().numpy(), h_table)
+        assert np.array_equal(Kp.double().cpu().numpy(), pool[0])
+        assert np.array_equal(Vp.double().cpu().numpy(), pool[1])
