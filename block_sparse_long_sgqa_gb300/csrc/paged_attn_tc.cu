@@ -327,7 +327,9 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       ok = publish(pc);
     }
     while (ok && nq < pub) ok = waited(pump());
-    if (lane == 0 && *up.flag != 0)
+    // Copies land before the CTA ends, whoever gives up and whenever: a role that has
+    // issued its last one may be done long before another one's wait runs out.
+    if (lane == 0)
       for (int i = 0; i < 2; ++i)
         if (loaded >> i & 1u) mbar_wait_drain(&q_full[i], (lph >> i) & 1u, a.status, 391);
   } else if (warp <= 2) {
@@ -375,7 +377,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         __syncwarp();
       }
     }
-    if (lane == 0 && *up.flag != 0)  // copies in flight land before the CTA ends
+    if (lane == 0)  // (as for Q above)
       for (int k = 0; k < NS; ++k) {
         const int uses = cnt / NS + (k < cnt % NS ? 1 : 0);
         if (uses > 0) mbar_wait_drain(&full[k], (uint32_t)((uses - 1) & 1), a.status, isK ? 392 : 393);

@@ -114,3 +114,37 @@ def test_captured_chain_of_steps(s, dtype):
         assert np.array_equal(table.cpu().numpy(), h_table)
         assert np.array_equal(Kp.double().cpu().numpy(), pool[0])
         assert np.array_equal(Vp.double().cpu().numpy(), pool[1])
+
+
+# ------------------------------------------------------------ giving up a wait
+def test_drains_do_not_hang_on_the_flag():
+    """A role whose copies are all issued leaves before another role gives up, so
+    it waits for them whether or not the flag is up by then."""
+    text = open(os.path.join(CSRC, "paged_attn_tc.cu")).read()
+    assert len(re.findall(r"mbar_wait_drain\(", text)) == 3 and "*up.flag != 0" not in text
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("q,kv", [([1], [100]), ([1, 1, 1], [250, 130, 7]), ([100], [150])])
+def test_stalled_wait_of_a_short_request(s, monkeypatch, d, q, kv):
+    """Requests of one or two key tiles, whose loads are all issued before the
+    products' wait runs out: the status says so, the next call is right."""
+    import test_paged
+
+    monkeypatch.setitem(test_paged.ATTN, "stall", (q, kv, 8, 2, d, 16, {}))
+    b, p, wide, K, V, q_start, kw = attn_case(s, "stall", "bf16")
+    a = dict(Q=wide.cuda(), K_pages=K.cuda(), V_pages=V.cuda(), page_table=dev(b.table),
+             q_start=dev(q_start), kv_len=dev(b.kv),
+             O=torch.full(wide.shape, 3.0, dtype=wide.dtype, device="cuda"),
+             lse=torch.full((p.n_q_heads, p.max_tokens), 7.0, device="cuda"),
+             ws=s.alloc_paged_workspace(p))
+    st = s.new_status()
+    for _ in range(3):
+        st[3] = s.DEBUG_STALL
+        s.sgqa_paged_attn(p, **a, status=st)
+        assert s.read_status(st) == (s.ERR_TIMEOUT, 220)
+        s.reset_status(st)
+        s.sgqa_paged_attn(p, **a, status=st)
+        assert status_of(s, st) == s.OK
+        check_attn(s, b, p, wide, K, V, q_start, kw, a["O"], a["lse"])
