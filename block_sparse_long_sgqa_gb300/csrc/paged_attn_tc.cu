@@ -163,6 +163,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   pdl_next();
   if (smem_u32(smem) & 1023u) {  // the operand tiles' swizzle needs it
+    pdl_wait();
+    if (threadIdx.x == 0) a.rec[blockIdx.x] = make_int4(0, 0, 0, 0);  // nothing to merge
     if (blockIdx.x == 0 && threadIdx.x == 0) report(a.status, SGQA_ERR_BOUNDS, 330);
     return;
   }

@@ -40,6 +40,21 @@ def test_no_restrict_behind_a_dependent_launch():
     assert seen >= 4
 
 
+def test_no_way_past_the_wait_or_the_record():
+    """Every way out of a kernel that others may depend on lies behind its wait, and
+    the attention kernels' ways out leave the record that the merge reads."""
+    seen = 0
+    for name in os.listdir(CSRC):
+        text = open(os.path.join(CSRC, name)).read()
+        for part in re.split(r"pdl_next\(\);", text)[1:]:
+            seen += 1
+            assert not re.search(r"\breturn\b", part.split("pdl_wait();")[0]), name
+    assert seen >= 6
+    text = open(os.path.join(CSRC, "paged_attn_tc.cu")).read()
+    early = re.search(r"& 1023u\) \{.*?return;", text, re.S).group(0)
+    assert early.index("pdl_wait()") < early.index("a.rec[blockIdx.x] = make_int4(0, 0, 0, 0)")
+
+
 @gpu
 @both
 def test_captured_chain_of_steps(s, dtype):
