@@ -433,7 +433,10 @@ SGQA_API int sgqa_page_plan(const sgqa_paged_params* p, const int32_t* q_len,
  * that several requests share must be given back once, by one of them.
  * SGQA_ERR_BOUNDS (keep_len outside [0, kv_len], kv_len above max_pages *
  * page_size, n_free outside [0, n_pages]) and SGQA_ERR_CAPACITY (more pages
- * than the stack's n_pages entries) change nothing but n_free_out = n_free. */
+ * than the stack's n_pages entries) change nothing but n_free_out = n_free.  A
+ * page number outside the pool among those given back is SGQA_ERR_BOUNDS too and
+ * gives nothing back: n_free_out = n_free and the stack stays, while the entries
+ * of free_pages behind its n_free[0] ones may have been overwritten. */
 SGQA_API int sgqa_page_release(const sgqa_paged_params* p, const int32_t* kv_len,
                                const int32_t* keep_len, const int32_t* page_table,
                                int32_t* free_pages, const int32_t* n_free, int32_t* n_free_out,

@@ -163,3 +163,59 @@ def test_stalled_wait_of_a_short_request(s, monkeypatch, d, q, kv):
         s.sgqa_paged_attn(p, **a, status=st)
         assert status_of(s, st) == s.OK
         check_attn(s, b, p, wide, K, V, q_start, kw, a["O"], a["lse"])
+
+
+# ------------------------------------------------------------------- release
+def run_release(s, b, kv, keep):
+    p = params(s, n_seqs=b.N, max_tokens=0, page_size=b.ps, n_pages=b.n_pages,
+               max_pages=b.max_pages)
+    free, nf, st = dev(b.free), dev([b.n_free]).int(), s.new_status()
+    out = torch.full_like(nf, 77)
+    s.sgqa_page_release(p, dev(kv).int(), dev(keep).int(), dev(b.table), free, nf, out, status=st)
+    return free.cpu().numpy(), out.item(), s.read_status(st)
+
+
+def release_case(name):
+    rng = np.random.default_rng(31)
+    n, kv_max, ps = {"one": (1, 9, 8), "some": (60, 300, 16), "tiles": (4500, 60, 8),
+                     "long": (40, 30000, 8), "one_long": (1, 600000, 8),
+                     "most": (2100, 6000, 8)}[name]
+    kv = rng.integers(1, kv_max, n)
+    kv[0] = kv_max
+    keep = np.where(rng.random(n) < 0.5, 0, rng.integers(0, kv + 1))
+    keep[0] = min(keep[0], 17)
+    return Batch(32, [0] * n, kv, ps, held_at="after"), kv, keep
+
+
+RELEASES = ["one", "some", "tiles", "long", "one_long", "most"]
+
+
+@gpu
+@pytest.mark.parametrize("name", RELEASES)
+def test_release_of_many_pages(s, name):
+    """Pages that requests keep are not looked at, whatever their numbers."""
+    b, kv, keep = release_case(name)
+    for i in range(b.N):
+        b.table[i, :ref.pages_of(int(keep[i]), b.ps)] = -1
+    want, n_free = ref.release(kv, keep, b.table, b.free, b.n_free, b.ps)
+    free, out, (code, _) = run_release(s, b, kv, keep)
+    assert code == s.OK
+    assert out == n_free and np.array_equal(free, want)
+
+
+@gpu
+@pytest.mark.parametrize("name", RELEASES)
+def test_release_of_a_bad_page_gives_nothing_back(s, name):
+    """A page number outside the pool among those given back refuses the call: the
+    stack and its count stay."""
+    b, kv, keep = release_case(name)
+    back = [(i, c) for i in range(b.N)
+            for c in range(ref.pages_of(int(keep[i]), b.ps), ref.pages_of(int(kv[i]), b.ps))]
+    table = b.table.copy()
+    for (i, c), bad in zip((back[0], back[-1], back[len(back) // 2], back[-len(back) // 3]),
+                           (-1, b.n_pages, (1 << 31) - 1, -(1 << 31))):
+        b.table = table.copy()
+        b.table[i, c] = bad
+        free, out, (code, detail) = run_release(s, b, kv, keep)
+        assert (code, detail) == (s.ERR_BOUNDS, 314)
+        assert out == b.n_free and np.array_equal(free[:out], b.free[:out])
