@@ -323,8 +323,10 @@ def paged_pool(p: PagedParams, device="cuda"):
 
 
 _TORCH_DTYPE = {BF16: torch.bfloat16, FP32: torch.float32}
-# torch.cuda's own wrappers of these cost 3 us and 0.3 us a call
-_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+# torch.cuda's own wrappers of these cost 3 us and 0.3 us a call.  (A torch without
+# CUDA has neither, and no tensor that a call would get as far as them with.)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _at(t, dtype, numel, dev, what):

@@ -2,6 +2,8 @@
 them, values and tables that the operators promise to leave alone, refusals."""
 import os
 import re
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -219,3 +221,26 @@ def test_release_of_a_bad_page_gives_nothing_back(s, name):
         free, out, (code, detail) = run_release(s, b, kv, keep)
         assert (code, detail) == (s.ERR_BOUNDS, 314)
         assert out == b.n_free and np.array_equal(free[:out], b.free[:out])
+
+
+# ---------------------------------------------------------- a torch without CUDA
+def test_host_entries_without_torch_cuda():
+    """Sizing, planning and argument checks need no CUDA build of torch."""
+    code = """
+import torch
+for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+from block_sparse_long_sgqa_gb300 import sgqa as s
+p = s.paged_params(3, 10, 8, 2, 64, 16, 20, 4)
+assert s.paged_workspace_bytes(p) > 0
+t = torch.zeros(20, dtype=torch.int32)
+try:
+    s.sgqa_page_release(p, t, t, t, t, t, t)
+except ValueError as e:
+    assert "CUDA" in str(e)
+else:
+    raise SystemExit("a CPU tensor was taken")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout + r.stderr
