@@ -723,6 +723,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       // part writes all of it
       const bool share = pc.single && n1 > 0;
       float g0, g1, lt = l, mm = m_used;
+      bool part0 = true, part1 = true;  // the row saw keys in the group's tiles
       if (share) {
         ok = o_done();
         if (!ok) break;
@@ -737,6 +738,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         g0 = m0 == ninf ? 0.0f : ex2(m0 - mm);
         g1 = m1 == ninf ? 0.0f : ex2(m1 - mm);
         lt = xsum[r] * g0 + xsum[BM + r] * g1;
+        part0 = m0 != ninf || lt != lt;
+        part1 = m1 != ninf || lt != lt;
       } else {
         g0 = grp == 0 ? 1.0f : 0.0f;
         g1 = 1.0f - g0;
@@ -774,8 +777,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              o[e] = __float_as_uint((g0 != 0.0f ? __uint_as_float(o[e]) * g0 : 0.0f) +
-                                     (g1 != 0.0f ? __uint_as_float(o1[e]) * g1 : 0.0f));
+              o[e] = __float_as_uint((part0 ? __uint_as_float(o[e]) * g0 : 0.0f) +
+                                     (part1 ? __uint_as_float(o1[e]) * g1 : 0.0f));
           } else if (pc.n > 0) {
             tmem_ld32(tO + c, o);
             tmem_wait_ld();

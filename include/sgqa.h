@@ -462,10 +462,12 @@ SGQA_API int sgqa_paged_append(const sgqa_paged_params* p, const void* K, const 
  * no row of an item (up to 256 neighbouring (token, head) rows) can see, have
  * no effect whatever they hold, and neither do page_table entries of pages
  * that hold only such positions.  A key or value that some rows of an item
- * see and others do not must be finite: 0 times a NaN is one.  A NaN among the
- * scores that a row sees makes its O and lse NaN.  bf16 runs on the tensor
- * cores (fp32 softmax and accumulation, the softmax weights rounded to bf16 for
- * their product with V); fp32 runs in fp32 throughout.
+ * see and others do not must be finite: 0 times a NaN is one.  A NaN or +infinity
+ * among the scores that a row sees makes its O and lse NaN, a NaN among the values
+ * that it sees that column of its O, whatever the weight; a row all of whose
+ * scores are -infinity is one that sees nothing.  bf16 runs on the tensor cores
+ * (fp32 softmax and accumulation, the softmax weights rounded to bf16 for their
+ * product with V); fp32 runs in fp32 throughout.  O and lse overlap no input.
  * Device checks (SGQA_ERR_BOUNDS): kv_len outside [0, max_pages * page_size]
  * and q_start that decreases or leaves [0, max_tokens] drop the request, a
  * page number outside the pool reads as zeros.  Results do not depend on

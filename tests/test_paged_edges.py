@@ -223,6 +223,36 @@ def test_release_of_a_bad_page_gives_nothing_back(s, name):
         assert out == b.n_free and np.array_equal(free[:out], b.free[:out])
 
 
+# ------------------------------------------------------------ values at the edge
+@gpu
+@both
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kv", [100, 256, 700, 9000])
+def test_nan_value_of_no_weight_is_seen(s, monkeypatch, dtype, d, kv):
+    """A NaN among the values that a row sees makes that column of its output NaN,
+    also where the weight, e^-200 of the row's, is 0 in 32 bits: in one tile, in
+    tiles of both groups and in parts that are merged.  lse and the other columns
+    are the ordinary ones."""
+    import test_paged
+
+    monkeypatch.setitem(test_paged.ATTN, "weightless", ([1, 1], [kv, 5], 8, 2, d, 16, {}))
+    b, p, wide, K, V, q_start, kw = attn_case(s, "weightless", dtype)
+    low = min(kv // 2, 128)  # keys before it have scores 200 below the others'
+    wide[0, :, 0] = 16.0
+    for j in range(kv):
+        K[b.table[0, j // 16], :, j % 16, 0] = 0.0 if j < low else 200.0 * np.sqrt(d) / 16
+    for j in (0, low // 2, low - 1):
+        at = (int(b.table[0, j // 16]), 1, j % 16, 3)
+        was = V[at].item()
+        V[at] = float("nan")
+        O, lse, code = run_attn(s, p, wide, K, V, b.table, q_start, b.kv)
+        V[at] = was
+        assert code == s.OK
+        assert torch.isnan(O[0, 4:, 3]).all(), j
+        O[0, 4:, 3] = run_attn(s, p, wide, K, V, b.table, q_start, b.kv)[0][0, 4:, 3]
+        check_attn(s, b, p, wide, K, V, q_start, kw, O, lse)
+
+
 # ---------------------------------------------------------- a torch without CUDA
 def test_host_entries_without_torch_cuda():
     """Sizing, planning and argument checks need no CUDA build of torch."""
