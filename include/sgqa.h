@@ -378,6 +378,10 @@ SGQA_API int sgqa_decode(const sgqa_params* p, const void* Q, const void* K, con
  * q_start[s] + i sits at position kv_len[s] - q_len[s] + i.  max_tokens is
  * the number of rows those tensors have, at least q_start[N]; rows from
  * q_start[N] on are padding.
+ * The entry points above work on the same pools: a request at a time, with
+ * page_table + s * max_pages for its page table, kv_len[s] for seq_kv and
+ * kv_len[s] - q_len[s] for q_offset (their own batch wants equal lengths and
+ * rows of exactly ceil(seq_kv / page_size) pages).
  * Supported: head_dim 64 and 128, page_size a multiple of 8, n_q_heads /
  * n_kv_heads up to 128, max_tokens up to 2^24, max_pages * page_size up to
  * 2^25 positions, n_pages * n_kv_heads * page_size and max_tokens * n_q_heads

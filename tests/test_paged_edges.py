@@ -253,6 +253,299 @@ def test_nan_value_of_no_weight_is_seen(s, monkeypatch, dtype, d, kv):
         check_attn(s, b, p, wide, K, V, q_start, kw, O, lse)
 
 
+def request_hit(p, q_start, i, g=None):
+    """[T][H] mask of request i's rows (of KV head g's heads)."""
+    G = p.n_q_heads // p.n_kv_heads
+    hit = torch.zeros(p.max_tokens, p.n_q_heads, dtype=torch.bool, device="cuda")
+    hit[q_start[i]:q_start[i + 1], slice(None) if g is None else slice(g * G, (g + 1) * G)] = True
+    return hit
+
+
+EDGE = ["decode", "decode_long", "few_g16", "chunk", "mixed_idle"]
+
+
+@gpu
+@both
+@pytest.mark.parametrize("name", EDGE)
+def test_scores_of_minus_infinity(s, name, dtype):
+    """Keys whose scores are -infinity have no weight; a row all of whose scores
+    are is one that sees nothing.  Other requests keep their bits."""
+    b, p, wide, K, V, q_start, kw = attn_case(s, name, dtype)
+    i = int(np.argmax(b.kv * (b.q > 0)))
+    rows = slice(int(q_start[i]), int(q_start[i + 1]))
+    wide[rows, :, 5] = wide[rows, :, 5].abs() + 0.5
+    first = run_attn(s, p, wide, K, V, b.table, q_start, b.kv)
+    n, hit = int(b.kv[i]), request_hit(p, q_start, i)
+    half = max(1, int(n - b.q[i]) // 2)
+    for upto in (half, n):
+        K2, K64 = K.clone(), K.clone()
+        for j in range(upto):
+            K2[b.table[i, j // b.ps], :, j % b.ps, 5] = -float("inf")
+            K64[b.table[i, j // b.ps], :, j % b.ps, 5] = -4096.0  # a weight below e^-100
+        O, lse, code = run_attn(s, p, wide, K2, V, b.table, q_start, b.kv)
+        assert code == s.OK
+        assert torch.equal(O[~hit], first[0][~hit]) and torch.equal(lse.T[~hit], first[1].T[~hit])
+        if upto == n:
+            assert (O[hit] == 0).all() and torch.isneginf(lse.T[hit]).all()
+        else:
+            check_attn(s, b, p, wide, K64, V, q_start, kw, O, lse)
+
+
+@gpu
+@both
+@pytest.mark.parametrize("name", ["decode", "decode_long", "few_g16", "decode_split_16"])
+def test_infinite_scores_and_values(s, name, dtype):
+    """A score of +infinity makes a row's O and lse NaN; an infinite value makes its
+    column of O infinite and leaves lse and the other columns.  Single tokens."""
+    b, p, wide, K, V, q_start, kw = attn_case(s, name, dtype)
+    i, g = int(np.argmax(b.kv * (b.q > 0))), p.n_kv_heads - 1
+    t, hit = int(q_start[i]), request_hit(p, q_start, i, g)
+    wide[t, :, 5] = wide[t, :, 5].abs() + 0.5
+    O, lse, code = run_attn(s, p, wide, K, V, b.table, q_start, b.kv)
+    for j in (0, int(b.kv[i]) // 2, int(b.kv[i]) - 1):
+        at = (int(b.table[i, j // b.ps]), g, j % b.ps, 5)
+        K2, V2 = K.clone(), V.clone()
+        K2[at] = float("inf")
+        Oi, li, code = run_attn(s, p, wide, K2, V, b.table, q_start, b.kv)
+        assert code == s.OK
+        assert torch.isnan(Oi[hit]).all() and torch.isnan(li.T[hit]).all()
+        assert torch.equal(Oi[~hit], O[~hit]) and torch.equal(li.T[~hit], lse.T[~hit])
+        V2[at] = -float("inf")
+        Oi, li, code = run_attn(s, p, wide, K, V2, b.table, q_start, b.kv)
+        assert code == s.OK
+        assert torch.isneginf(Oi[hit][:, 5]).all()
+        Oi[..., 5][hit] = O[..., 5][hit]
+        assert torch.equal(Oi, O) and torch.equal(li, lse)
+
+
+# --------------------------------------------- what lies before a window, bad pages
+WINDOWS = {
+    # single tokens and drafts whose windows begin at every offset of a page
+    "one": ([1] * 40, [300 + i for i in range(40)], 16, 2, 128, 24, dict(window=100)),
+    "one_d64": ([1] * 40, [250 + i for i in range(40)], 32, 2, 64, 32, dict(window=130)),
+    "drafts": ([5] * 20, [700 + i for i in range(20)], 16, 2, 128, 16, dict(window=65)),
+    "chunks": ([150, 80, 1, 33], [900, 505, 400, 290], 16, 4, 128, 40, dict(window=77)),
+    "chunks_d64": ([300, 41], [1000, 600], 8, 1, 64, 64, dict(window=200)),
+    "long": ([1, 1], [30000, 20001], 8, 1, 128, 64, dict(window=9000)),
+    "first": ([1, 20], [600, 700], 8, 2, 64, 8, dict(window=1)),
+}
+
+
+@gpu
+@both
+@pytest.mark.parametrize("name", WINDOWS)
+def test_what_lies_before_a_window_has_no_effect(s, monkeypatch, name, dtype):
+    """Keys and values before the first position that a request's rows see hold NaN
+    and infinities, and the pages that lie wholly before it have no valid number."""
+    import test_paged
+
+    monkeypatch.setitem(test_paged.ATTN, "before", WINDOWS[name])
+    b, p, wide, K, V, q_start, kw = attn_case(s, "before", dtype)
+    bad = [-1, b.n_pages, -(1 << 31), (1 << 31) - 1]
+    for i in range(b.N):
+        lo = max(0, int(b.kv[i] - b.q[i]) + 1 - p.window)
+        for j in range(lo):
+            K[b.table[i, j // b.ps], :, j % b.ps] = float("nan") if j % 3 else float("inf")
+            V[b.table[i, j // b.ps], :, j % b.ps] = float("nan") if j % 2 else -float("inf")
+        b.table[i, :lo // b.ps] = [bad[c % 4] for c in range(lo // b.ps)]
+    O, lse, code = run_attn(s, p, wide, K, V, b.table, q_start, b.kv)
+    assert code == s.OK
+    check_attn(s, b, p, wide, K, V, q_start, kw, O, lse)
+
+
+@gpu
+@both
+@pytest.mark.parametrize("d", [64, 128])
+def test_what_other_items_see_has_no_effect(s, monkeypatch, dtype, d):
+    """A NaN that only the first rows of a windowed chunk see stays within 256 (token,
+    head) rows of them."""
+    import test_paged
+
+    monkeypatch.setitem(test_paged.ATTN, "items", ([400], [900], 8, 2, d, 16, dict(window=90)))
+    b, p, wide, K, V, q_start, kw = attn_case(s, "items", dtype)
+    O, lse, _ = run_attn(s, p, wide, K, V, b.table, q_start, b.kv)
+    j = 500 + 1 - 90  # the first position that token 0 (at 500) sees, and only it
+    K[b.table[0, j // 16], :, j % 16] = float("nan")
+    V[b.table[0, j // 16], :, j % 16] = float("nan")
+    On, ln, code = run_attn(s, p, wide, K, V, b.table, q_start, b.kv)
+    assert code == s.OK
+    assert torch.isnan(On[0]).all() and torch.isnan(ln[:, 0]).all()
+    assert torch.equal(On[64:], O[64:]) and torch.equal(ln[:, 64:], lse[:, 64:])
+    assert torch.equal(ln[:, 1:], lse[:, 1:])  # scores that a row does not see are left out
+
+
+@gpu
+@both
+@pytest.mark.parametrize("name", ["decode_long", "chunk", "mixed_idle", "few_two_tokens", "window"])
+def test_bad_pages_read_as_zeros(s, name, dtype):
+    b, p, wide, K, V, q_start, kw = attn_case(s, name, dtype)
+    i = int(np.argmax(b.kv * (b.q > 0)))
+    c = ref.pages_of(int(b.kv[i]), b.ps) - 2
+    zero = torch.zeros_like(K[:1])
+    K64, V64, good = torch.cat([K, zero]), torch.cat([V, zero]), b.table.copy()
+    for bad in (-1, b.n_pages, -(1 << 31), (1 << 31) - 1):
+        b.table = good.copy()
+        b.table[i, c] = bad
+        O, lse, code = run_attn(s, p, wide, K, V, b.table, q_start, b.kv)
+        assert code == s.ERR_BOUNDS
+        b.table[i, c] = b.n_pages  # the zero page of the 64-bit form
+        check_attn(s, b, p, wide, K64, V64, q_start, kw, O, lse)
+
+
+# ------------------------------------------------------------------- large ones
+@gpu
+@both
+def test_waves_among_other_requests(s, dtype):
+    """Requests that go out in waves beside single tokens, an idle one and a short
+    prompt; checked on spread rows."""
+    d, hk, ps = 128, 8, 64
+    H = 64 if dtype == "bf16" else 16
+    b = Batch(8, [1, 700, 0, 650, 30, 1], [3000, 20011, 50, 15000, 30, 9000], ps, held_at="after")
+    q_start = np.concatenate([[0], np.cumsum(b.q)]).astype(np.int32)
+    T = int(q_start[-1]) + 5
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    p = params(s, n_seqs=b.N, max_tokens=T, n_q_heads=H, n_kv_heads=hk, head_dim=d, page_size=ps,
+               n_pages=b.n_pages, max_pages=b.max_pages,
+               dtype=s.BF16 if dtype == "bf16" else s.FP32)
+    torch.manual_seed(3)
+    Q = torch.randn(T, H, d, device="cuda").to(dt)
+    K, V = (torch.randn(b.n_pages, hk, ps, d, device="cuda").to(dt) for _ in "KV")
+    O, lse, code = run_attn(s, p, Q.cpu(), K, V, b.table, q_start, b.kv)
+    assert code == s.OK
+    O, lse = O.double().cpu().numpy(), lse.double().cpu().numpy()
+    assert (O[-5:] == 3.0).all() and (lse[:, -5:] == 7.0).all()
+    assert np.isfinite(O).all() and np.isfinite(lse).all()
+    Kn, Vn, Qn = (x.double().cpu().numpy() for x in (K, V, Q))
+    for r in range(b.N):
+        for i in sorted({0, 1, 31, 32, 333, int(b.q[r]) - 1}):
+            if not 0 <= i < int(b.q[r]):
+                continue
+            t, n = int(q_start[r]) + i, int(b.kv[r] - b.q[r]) + i + 1
+            R, z, tO, tl, _ = ref.attention(Qn[t:t + 1], Kn, Vn, ps, b.table[r:r + 1], [0, 1], [n],
+                                            ref.default_scale(d), True, 0, dtype == "bf16")
+            assert (np.abs(O[t] - R[0]) <= tO[0]).all(), (r, i)
+            assert (np.abs(lse[:, t] - z[:, 0]) <= tl[:, 0]).all(), (r, i)
+
+
+@gpu
+@pytest.mark.parametrize("T", [1, 150])
+def test_fp32_offsets_past_4_gib(s, T):
+    """fp32 pages at the far end of a pool of more than 4 GiB, by the kernel for few
+    rows and the one for many."""
+    d, hk, H, ps, n_pages = 128, 8, 16, 64, 20000  # 5.2 GB for K, as much for V
+    p = params(s, n_seqs=1, max_tokens=T, n_q_heads=H, n_kv_heads=hk, head_dim=d, page_size=ps,
+               n_pages=n_pages, max_pages=3, dtype=s.FP32)
+    Kp, Vp = (torch.zeros(n_pages, hk, ps, d, device="cuda") for _ in "KV")
+    torch.manual_seed(4)
+    K, V = (torch.randn(150, hk, d, device="cuda") for _ in "KV")
+    Q = torch.randn(T, H, d, device="cuda")
+    table = np.array([[n_pages - 1, 2, n_pages - 2]], np.int32)
+    pos = np.arange(150)
+    slots = table[0, pos // ps].astype(np.int64) * ps + pos % ps
+    st = s.new_status()
+    pa = params(s, n_seqs=1, max_tokens=150, n_q_heads=H, n_kv_heads=hk, head_dim=d, page_size=ps,
+                n_pages=n_pages, max_pages=3, dtype=s.FP32)
+    s.sgqa_paged_append(pa, K, V, dev(slots), Kp, Vp, status=st)
+    O, lse = torch.zeros_like(Q), torch.zeros(H, T, device="cuda")
+    s.sgqa_paged_attn(p, Q, Kp, Vp, dev(table), dev(np.array([0, T], np.int32)),
+                      dev(np.array([150], np.int32)), O, lse, s.alloc_paged_workspace(p), status=st)
+    assert status_of(s, st) == s.OK
+    assert torch.equal(Kp[n_pages - 1].transpose(0, 1), K[:64])
+    used = Kp.flatten(1).any(1).nonzero().flatten().tolist()
+    assert used == [2, n_pages - 2, n_pages - 1]
+    Kl, Vl = (x.double().cpu().numpy().transpose(1, 0, 2)[None] for x in (K, V))
+    R, z, tO, tl, _ = ref.attention(Q.double().cpu().numpy(), Kl, Vl, 150, np.zeros((1, 1), int),
+                                    [0, T], [150], ref.default_scale(d), True, 0, False)
+    assert (np.abs(O.double().cpu().numpy() - R) <= tO).all()
+    assert (np.abs(lse.double().cpu().numpy() - z) <= tl).all()
+
+
+# ------------------------------------------- the sparse layer on the same pages
+@gpu
+def test_sparse_layer_on_planned_pages(s):
+    """A ragged batch through both kinds of layer over pools and tables that the
+    plan and the append made: the sparse layer takes a request at a time, on its row
+    of the page table, with the request's length as seq_kv.  Prompts, then a
+    decode step, against the oracle; the dense layer's decode step beside it."""
+    import oracle
+    from block_sparse_long_sgqa_gb300 import synth
+    from helpers import clear_margin, r3_check
+
+    ps, lens = 16, [700, 333, 41]
+    wls = [synth.WORKLOADS["gqa_32k"].replace(name="planned", seq_q=n + 1, seq_kv=n + 1,
+                                              topk_tokens=128, seed=77 + n) for n in lens]
+    inp = [synth.make_inputs(w) for w in wls]
+    rows = lambda x: torch.from_numpy(np.ascontiguousarray(x).view(np.int16)).cuda().view(torch.bfloat16)
+    H, hk, d = wls[0].n_q_heads, wls[0].n_kv_heads, wls[0].head_dim
+    N, n_pages, max_pages, T = len(lens), 90, 60, sum(lens) + 9
+    i32 = dict(dtype=torch.int32, device="cuda")
+    free = torch.randperm(n_pages, generator=torch.Generator().manual_seed(3)).int().cuda()
+    nf, nf2 = torch.full((1,), n_pages, **i32), torch.zeros(1, **i32)
+    table, st = torch.full((N, max_pages), -1, **i32), s.new_status()
+    Kp, Vp = (torch.full((n_pages, hk, ps, d), float("nan"), device="cuda").bfloat16() for _ in "kv")
+
+    def step(q, kv, T, parts):
+        """Plans and appends one step; parts(name): the rows of all requests."""
+        pp = params(s, n_seqs=N, max_tokens=T, n_q_heads=H, n_kv_heads=hk, head_dim=d,
+                    page_size=ps, n_pages=n_pages, max_pages=max_pages)
+        q_start, pos = torch.zeros(N + 1, **i32), torch.zeros(T, **i32)
+        slots = torch.zeros(T, dtype=torch.int64, device="cuda")
+        s.sgqa_page_plan(pp, dev(q).int(), dev(kv).int(), free, nf, table, q_start, slots, pos, nf2,
+                         status=st)
+        nf.copy_(nf2)
+        pad = T - sum(q)
+        x = {k: torch.cat([parts(k), torch.zeros(pad, (H if k == "Q" else hk), d, device="cuda",
+                                                 dtype=torch.bfloat16)]) for k in "QKV"}
+        s.sgqa_paged_append(pp, x["K"], x["V"], slots, Kp, Vp, status=st)
+        return pp, q_start, x["Q"]
+
+    def check(O, lse, i, r, q_offset):
+        w = wls[i].replace(seq_q=len(r), q_offset=q_offset)
+        Qf, Kf, Vf = (synth.widen(inp[i][k]) for k in "QKV")
+        n = q_offset + len(r)
+        w = w.replace(seq_kv=n)
+        S, _, O64, l64 = oracle.prefill_rows(Qf[q_offset:n], Kf[:n], Vf[:n], q_offset, w.block_size,
+                                             w.k_blocks, r)
+        mask = np.repeat(clear_margin(S, w, r).T, H // hk, axis=1)
+        assert mask.mean() >= 0.5
+        r3_check(O.float().cpu().numpy(), lse.cpu().numpy(), O64, l64, mask)
+
+    # the prompts
+    step(lens, lens, T, lambda k: torch.cat([rows(x[k][:n]) for x, n in zip(inp, lens)]))
+    for i, n in enumerate(lens):
+        p = s.params_for(wls[i].replace(seq_q=n, seq_kv=n, page_size=ps))
+        O, lse = s.alloc_outputs(p)
+        s.sgqa_prefill(p, rows(inp[i]["Q"][:n]), Kp, Vp, s.kbar_empty(p), O, lse,
+                       s.alloc_workspace(p, s.WS_PREFILL), page_table=table[i], status=st)
+        assert status_of(s, st) == s.OK
+        check(O, lse, i, np.arange(n, dtype=np.int32), 0)
+    # a decode step of all of them
+    after = [n + 1 for n in lens]
+    pp, q_start, Q = step([1] * N, after, N + 2, lambda k: torch.cat(
+        [rows(x[k][n:n + 1]) for x, n in zip(inp, lens)]))
+    for i, n in enumerate(lens):
+        p = s.params_for(wls[i].replace(seq_q=1, q_offset=n, page_size=ps))
+        O, lse = s.alloc_outputs(p)
+        cache = s.KeyCache(p, cap_blocks=(n + 1) // wls[i].block_size + 64)
+        s.sgqa_decode(p, Q[i:i + 1].contiguous(), Kp, Vp, cache, O, lse,
+                      s.alloc_workspace(p, s.WS_DECODE), page_table=table[i], status=st)
+        assert status_of(s, st) == s.OK
+        check(O, lse, i, np.arange(1, dtype=np.int32), n)
+    O, lse = torch.zeros_like(Q), torch.zeros(H, N + 2, device="cuda")
+    s.sgqa_paged_attn(pp, Q, Kp, Vp, table, q_start, dev(after).int(), O, lse,
+                      s.alloc_paged_workspace(pp), status=st)
+    assert status_of(s, st) == s.OK
+    big = max(after)
+    K, V = np.zeros((N, hk, big, d)), np.zeros((N, hk, big, d))
+    for i, n in enumerate(after):
+        for X, k in ((K, "K"), (V, "V")):
+            X[i, :, :n] = synth.widen(inp[i][k]).transpose(1, 0, 2)[:, :n]
+    R, z, tO, tl, _ = ref.attention(Q[:N].double().cpu().numpy(), K, V, big, np.arange(N)[:, None],
+                                    np.arange(N + 1), after, ref.default_scale(d), True, 0, True)
+    assert (np.abs(O[:N].double().cpu().numpy() - R) <= tO).all()
+    assert (np.abs(lse[:, :N].double().cpu().numpy() - z) <= tl).all()
+
+
 # ---------------------------------------------------------- a torch without CUDA
 def test_host_entries_without_torch_cuda():
     """Sizing, planning and argument checks need no CUDA build of torch."""
