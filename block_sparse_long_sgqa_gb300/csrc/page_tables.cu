@@ -10,7 +10,7 @@
 // from L2) and then serves an equal range of tokens, finding a token's request
 // by bisection of the sums in shared memory.  The work is a few bytes per
 // token (1.6 MB for 129K of them, 0.2 us at the copy rate); what bounds a call is
-// the launch and the chain of trips to memory: 3.7 us for 256 requests of one
+// the launch and the chain of trips to memory: 3.8 us for 256 requests of one
 // token, 5.0 for 512 requests and 129K tokens, in a row of such calls.
 #include "paged.h"
 

@@ -13,7 +13,7 @@
 // 1.2 for the scalar one.  What bounds it: the FMA pipe is 60 % busy and shared memory 74
 // % (3.1 wavefronts a read) with four warps a scheduler, which registers and shared memory
 // both allow and no more: 2656 tokens of 32 heads of 128 on contexts of 500 to 3000 keys
-// 2367 us, 38 of the 74 TFLOP/s of the pipe.  8 rows a thread halves the reads but leaves
+// 2349 us, 38 of the 74 TFLOP/s of the pipe.  8 rows a thread halves the reads but leaves
 // two warps a scheduler: 2637 us.  K and V copied at the tile's start: 70 us more.
 // paged_line.cuh lays the work out over two CTAs per SM; every warp walks it,
 // so that a CTA needs no hand-over between its warps.
@@ -257,10 +257,10 @@ __device__ __noinline__ void simt_piece(const SimtArgs& a, const Piece pc, float
 // columns; the parts are added and dealt out by halves, so that the lane ends with KL
 // keys of one row.  O: a lane has 4 columns of every row (d = 64: of every other R / 2).
 // What bounds it is reads of shared memory and instructions beside the copies: 16
-// requests of 3000 keys, 32 on 4 heads of 128, 55 us against 129 with the tiles above
-// (195 MB: 29 us); two of 110000 keys 173 us against 514 (0.90 GB: 133 us).  One row and
-// two keys a lane, with no sum over lanes: 70 us; 8 warps of d = 128 for 12: 58 us;
-// three stages for two: 2 us more; P stored in pairs, for fewer moves: 2 us more.
+// requests of 2000 to 4000 keys, 32 on 4 heads of 128, 50 us against 180 with the tiles
+// above (188 MB: 28 us); two of 110000 keys 169 us against 729 (0.93 GB: 137 us).  When
+// the first took 55: one row and two keys a lane, with no sum over lanes, 70 us; 8 warps
+// of d = 128 for 12, 58 us; three stages for two, or P stored in pairs, 2 us more.
 template <int D, int R_>
 struct Few {
   static constexpr int R = R_, NTH = D == 128 ? 384 : 256, WARPS = NTH / 32, WK = 8, STAGES = 2;
@@ -526,7 +526,8 @@ __global__ void __launch_bounds__((Few<D, R>::NTH), (Few<D, R>::PER_SM))
 }
 
 // Rows per item: 8 or 16 when the requests have on average at most that many and a group
-// fits (one token each: 55 and 129 us for 16 requests of 3000 keys, see above), else 64.
+// fits (one token each: 50 and 180 us for 16 requests of 2000 to 4000 keys), else 64.
+// The host knows the rows of the buffers, not the lengths, so padding rows count.
 int rows_of(const PagedDims& pd) {
   for (int R : {8, 16})
     if (pd.G <= R && (int64_t)pd.T * pd.G <= (int64_t)R * pd.N) return R;
@@ -568,10 +569,10 @@ int launch_paged_simt(const PagedDims& pd, const PagedAttnArgs& pa, void* ws, cu
   a.tpm = R / a.heads;
   a.tiles_per_item = 1;
   a.tile_rows = 0;
-  // (3 chunks of 100 to 401 tokens of 4 heads of 64: 49.8 us, with 2 52.3, with 3 52.7;
-  // 16 single tokens over 3000 keys: 54.4 with 2, 54.8 with 1)
+  // (3 chunks of 100 to 401 tokens of 4 heads of 64: 47.1 us, with 2 49.9, with 3 50.5;
+  // 16 single tokens over 3000 keys: 51.4 with 2, 52.1 with 1, 53.7 with 3)
   a.over = R == 64 && pd.window == 0 ? 1 : 2;
-  // four contexts of up to 700 keys 16.5 us (whole = 2: 18.4)
+  // four contexts of up to 700 keys 12.8 us (2: 13.6)
   a.whole = a.part = 1;
   a.Q = static_cast<const float*>(pa.Q);
   a.K = static_cast<const float*>(pa.K);

@@ -3,7 +3,10 @@
 // Online softmax in one pass over a request's keys, 128 at a time: S = Q K^T
 // into tensor memory, P = 2^(S scale log2 e - m) rounded to bf16 (m: a running
 // reference maximum, raised only when a tile exceeds it by much), O += P V, and
-// at the end O / l with l the sum of P in fp32.
+// at the end O / l with l the sum of P in fp32.  P is rounded because both operands
+// of a product have one type: each weight is off by at most 2^-8 of itself, which for
+// random values adds 1.5e-3 of O (root mean square) to the 1.65e-3 that O's own rounding
+// costs; two bf16 terms of P would double P V.
 //
 // A query tile is 128 / G tokens with their G query heads as the M = 128 rows of
 // every product, so each K and V tile that is read serves the whole KV group.
@@ -874,10 +877,11 @@ int launch_paged_tc(const PagedDims& pd, const PagedAttnArgs& pa, void* ws, cuda
   a.tpm = BM / pd.G;
   a.tiles_per_item = 2;
   a.tile_rows = BM;
-  a.over = 3;  // (2: mixed chunk 106.8 us for 104.8; 4: 105.7)
-  // 0.8 us a tile, 4 us for a merge: four contexts of 300 to 2047 keys 14.1 us, of 1000
-  // to 5000 16.3 (8 and 6: 14.7 and 18.0; 4 and 3: 15.2 and 17.2).  Without a merge when
-  // no cache is longer than 8 tiles: 1000 keys 12.5 us, against 12.9.
+  a.over = 3;  // (2 to 4 are alike: mixed chunks 100, 99, 99 us, 64 ragged contexts 358, 361, 360)
+  // 0.8 us a tile, 4 us for a merge: four contexts of 300 to 2047 keys 14.8 us, of 1000
+  // to 5000 16.7 (8 and 6: 15.5 and 16.5; 4 and 3: 15.4 and 17.3).  Without a merge where
+  // the page table holds at most 8 tiles, so that no cache can be longer: four contexts
+  // of 1000 keys 13.2 us, against 14.2.
   a.whole = a.part = 4;
   a.uncut = pd.cap <= 8 * KB;
   a.O = static_cast<__nv_bfloat16*>(pa.O);
