@@ -48,6 +48,12 @@ int launch_paged_simt(const PagedDims& pd, const PagedAttnArgs& a, void* ws, cud
 size_t paged_tc_ws_bytes(const PagedDims& pd);
 int launch_paged_tc(const PagedDims& pd, const PagedAttnArgs& a, void* ws, cudaStream_t st);
 
+// Whether two buffers share a byte (a NULL or empty one shares none).
+inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a != nullptr && b != nullptr && na > 0 && nb > 0 && (x < y ? y - x < na : x - y < nb);
+}
+
 // Launches in a row: each kernel lets the next one be scheduled from its start on
 // (pdl_next) and, before it touches memory that another kernel may still read or write,
 // waits until the one before it is complete (pdl_wait).  The next launch's latency and

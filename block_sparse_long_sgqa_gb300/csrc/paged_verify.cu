@@ -223,7 +223,6 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_verify(const VerifyArgs a) {
   if (rank == 0 && tid == 0) {
     if (bad) report(a.status, SGQA_ERR_BOUNDS, 362);
     a.n_accepted[s] = n;
-    a.keep_len[s] = kv - k + n;
   }
 
   // ---- this CTA's units, and each warp's range of them
@@ -293,7 +292,12 @@ __global__ void __launch_bounds__(NT, 1024 / NT) k_verify(const VerifyArgs a) {
     const Pair mine = warp_sum(joined(sum));
     if (lane == 0) sh.warp[warp] = mine;
     __syncthreads();
-    if (round == 0) cluster.barrier_wait();  // all CTAs have begun
+    if (round == 0) {
+      cluster.barrier_wait();  // all CTAs have begun
+      // (not before: keep_len may be kv_len, and a CTA that read the new length could take
+      // the request for one that does not fit and leave the cluster)
+      if (rank == 0 && tid == 0) a.keep_len[s] = kv - k + n;
+    }
     if (tid < C) {
       Pair t = none;
 #pragma unroll
@@ -439,6 +443,22 @@ extern "C" SGQA_API int sgqa_draft_verify(
   const unsigned e = p->dtype == SGQA_BF16 ? 2 : 4;
   if (reinterpret_cast<uintptr_t>(P) % e || reinterpret_cast<uintptr_t>(D) % e)
     return SGQA_ERR_ALIGNMENT;
+  // Outputs on inputs: the CTAs of a request each read its lengths and drafts for themselves,
+  // and have to come to the same verdict whatever other requests have written by then.
+  const size_t n = (size_t)p->n_seqs * 4, t = (size_t)p->max_tokens * 4;
+  auto rows = [&](int32_t stride) -> size_t {
+    if (p->max_tokens == 0) return 0;
+    return ((size_t)(p->max_tokens - 1) * (stride ? stride : p->vocab) + p->vocab) * e;
+  };
+  int32_t* const outs[3] = {n_accepted, next_token, keep_len};
+  for (int i = 0; i < 3; ++i) {
+    if (overlap(outs[i], n, q_start, n + 4) || overlap(outs[i], n, tokens, t) ||
+        overlap(outs[i], n, u, t) || overlap(outs[i], n, u_next, n) ||
+        overlap(outs[i], n, P, rows(p->p_stride)) || overlap(outs[i], n, D, rows(p->d_stride)) ||
+        (outs[i] != kv_len ? overlap(outs[i], n, kv_len, n) : outs[i] != keep_len) ||
+        overlap(outs[i], n, outs[(i + 1) % 3], n))
+      return SGQA_ERR_INVALID_ARG;
+  }
   VerifyArgs a;
   a.P = P;
   a.D = D;

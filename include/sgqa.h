@@ -668,7 +668,9 @@ SGQA_API int sgqa_evict_move(const sgqa_paged_params* p, int32_t budget,
  * counts as 0, a NaN turns the draft down or takes the last token with a weight.
  * n_accepted[s] = i, keep_len[s] = kv_len[s] - k + i (the cache without the drafts that were
  * turned down: keep_len of sgqa_page_release); a request without tokens gets
- * n_accepted = 0, next_token = -1, keep_len = kv_len.  Products and sums in 64
+ * n_accepted = 0, next_token = -1, keep_len = kv_len.  keep_len may be kv_len itself
+ * (lengths updated in place); otherwise the three outputs overlap neither an input nor
+ * one another (INVALID_ARG).  Products and sums in 64
  * bits or pairs of 32.  P and D hold finite values (negative ones and NaN count as 0),
  * need not sum to 1, and are read as given.  A row without any positive w
  * falls back to P, then to -1 (SGQA_ERR_BOUNDS).  Device checks

@@ -1,0 +1,80 @@
+"""Calls of the operators around the paged cache that their documentation allows or
+refuses: outputs on inputs, host threads at once, forms that the ordinary sizes do not reach."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from test_cache_ops import VERIFIES, VerifyCase, dev
+
+gpu = pytest.mark.gpu
+# Addresses that nothing may read: where a refusal were missing, the call would.
+no_gpu = pytest.mark.skipif(torch.cuda.is_available(), reason="calls with made-up addresses")
+
+
+@pytest.fixture(scope="module")
+def s():
+    from block_sparse_long_sgqa_gb300 import sgqa
+
+    return sgqa
+
+
+def clashes(inputs, outputs, allowed=()):
+    """(output, address) for each output placed on each other buffer: at its start, and so
+    that its last or first word is the other's first or last."""
+    sizes = {**inputs, **outputs}
+    base = {k: (i + 1) << 32 for i, k in enumerate(sizes)}
+    for o in outputs:
+        for b in sizes:
+            if b == o:
+                continue
+            places = [base[b] - outputs[o] + 4, base[b] + sizes[b] - 4]
+            if (o, b) not in allowed:
+                places.append(base[b])
+            for x in places:
+                yield o, b, {**base, o: x}
+
+
+# -------------------------------------------------------------- verification
+@no_gpu
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_verify_refuses_outputs_on_inputs(s, dtype):
+    n, t, v, e = 5, 17, 100, 4 if dtype == "fp32" else 2
+    p = s.verify_params(n, t, v, s.FP32 if e == 4 else s.BF16, p_stride=104, d_stride=112)
+    inputs = dict(P=((t - 1) * 104 + v) * e, D=((t - 1) * 112 + v) * e, tokens=4 * t, q_start=4 * n + 4,
+                  kv_len=4 * n, u=4 * t, u_next=4 * n)
+    outputs = dict(n_accepted=4 * n, next_token=4 * n, keep_len=4 * n)
+    for o, b, at in clashes(inputs, outputs, allowed=[("keep_len", "kv_len")]):
+        rc = s._lib.sgqa_draft_verify(ctypes.byref(p), *at.values(), None, None)
+        assert rc == s.ERR_INVALID_ARG, (o, b)
+
+
+@gpu
+@pytest.mark.parametrize("name", VERIFIES)
+def test_verify_lengths_in_place(s, name):
+    """keep_len on kv_len, from caches no longer than the drafts (so that the new length would
+    not hold them): as with a buffer of its own."""
+    c = VerifyCase(s, name)
+    c.kv = np.diff(c.q_start).astype(np.int32)
+    for _ in range(10):
+        kv = dev(c.kv).clone()
+        c.out["keep_len"] = kv
+        assert c.run(s, kv_len=kv) == s.OK
+        c.check()
+
+
+@gpu
+def test_verify_lengths_in_place_many(s):
+    """The same with more requests than fit the SMs at a time."""
+    VERIFIES["crowd"] = ([2] * 400, 20000, True, "bf16", 0)
+    try:
+        c = VerifyCase(s, "crowd")
+    finally:
+        del VERIFIES["crowd"]
+    c.kv = np.diff(c.q_start).astype(np.int32)
+    for _ in range(5):
+        kv = dev(c.kv).clone()
+        c.out["keep_len"] = kv
+        assert c.run(s, kv_len=kv) == s.OK
+        c.check()
