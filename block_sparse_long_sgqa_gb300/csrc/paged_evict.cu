@@ -308,9 +308,11 @@ __global__ void __launch_bounds__(NT) k_evict_plan(const __grid_constant__ PlanA
 
 template <bool HELD, int C>
 int launch_plan(const PlanArgs& a, size_t smem, cudaStream_t st) {
-  if (smem + sizeof(PlanShared) > 48 * 1024 &&  // (less needs no leave)
+  // (less needs no leave; always the most that a call can ask for: the limit belongs to the
+  // process, and another thread's smaller call must not lower it before this one's launch)
+  if (smem + sizeof(PlanShared) > 48 * 1024 &&
       cudaFuncSetAttribute(k_evict_plan<HELD, C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)smem) != cudaSuccess)
+                           kMostKeys * 4) != cudaSuccess)
     return SGQA_ERR_CUDA;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -1,12 +1,14 @@
 """Calls of the operators around the paged cache that their documentation allows or
 refuses: outputs on inputs, host threads at once, forms that the ordinary sizes do not reach."""
 import ctypes
+import threading
 
 import numpy as np
 import pytest
 import torch
 
 from test_cache_ops import VERIFIES, VerifyCase, dev
+from test_paged import params, status_of
 
 gpu = pytest.mark.gpu
 # Addresses that nothing may read: where a refusal were missing, the call would.
@@ -78,3 +80,42 @@ def test_verify_lengths_in_place_many(s):
         c.out["keep_len"] = kv
         assert c.run(s, kv_len=kv) == s.OK
         c.check()
+
+
+# ------------------------------------------------------------------ eviction
+@gpu
+def test_plans_of_two_host_threads(s):
+    """Tables of different widths, planned from two threads at once: the shared memory that one
+    call asks for does not depend on the other's."""
+    n, hk, ps, kv, budget, rounds = 38, 4, 64, 100, 60, 3000  # a block a (request, group)
+    fail, got, gate = [], [None, None], threading.Barrier(2)
+
+    def work(i, max_pages):
+        p = params(s, n_seqs=n, max_tokens=0, n_q_heads=hk, n_kv_heads=hk, page_size=ps, n_pages=2,
+                   max_pages=max_pages)
+        i32 = dict(dtype=torch.int32, device="cuda")
+        with torch.cuda.stream(torch.cuda.Stream()):
+            mass = torch.arange(2 * hk * ps, dtype=torch.float32, device="cuda")
+            table = torch.zeros(n, max_pages, **i32)
+            table[:, 1] = 1
+            lens = torch.full((n,), kv, **i32)
+            out = [torch.zeros(n, hk, **i32), torch.zeros(n, hk, budget, 2, **i32), torch.zeros(n, **i32)]
+            status = s.new_status()
+            gate.wait()
+            try:
+                for _ in range(rounds):
+                    s.sgqa_evict_plan(p, mass, table, lens, *out, budget=budget, status=status)
+                assert status_of(s, status) == s.OK
+                got[i] = [x.cpu() for x in out]
+            except Exception as e:
+                fail.append(e)
+    # 12800 and 32768 keys a block: 50 and 128 KB
+    threads = [threading.Thread(target=work, args=a) for a in ((0, 200), (1, 512))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not fail, fail
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    assert (got[0][0] == kv - budget).all()
