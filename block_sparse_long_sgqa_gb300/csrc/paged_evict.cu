@@ -460,6 +460,22 @@ SGQA_API int sgqa_evict_plan(const sgqa_paged_params* p, int32_t budget, int32_t
       moves == nullptr || kv_len_out == nullptr || kv_len_out == kv_len)
     return SGQA_ERR_INVALID_ARG;
   if (!aligned16(mass_pages) || !aligned16(pos_pages)) return SGQA_ERR_ALIGNMENT;
+  // Outputs on inputs: the CTAs of a (request, group) read its length and its entries each for
+  // itself, and more than once, while other (request, group)s write theirs.
+  const size_t seqs = (size_t)pd.N * 4, units = seqs * pd.Hkv;
+  const size_t entries = (size_t)pd.n_pages * pd.Hkv * pd.ps * 4;
+  const struct {
+    const void* p;
+    size_t n;
+  } outs[3] = {{n_moves, units}, {moves, units * 2 * budget}, {kv_len_out, seqs}};
+  for (int i = 0; i < 3; ++i) {
+    const auto& o = outs[i];
+    if (overlap(o.p, o.n, kv_len, seqs) || overlap(o.p, o.n, next_pos, seqs) ||
+        overlap(o.p, o.n, page_table, seqs * pd.max_pages) ||
+        overlap(o.p, o.n, mass_pages, entries) || overlap(o.p, o.n, pos_pages, entries) ||
+        overlap(o.p, o.n, outs[(i + 1) % 3].p, outs[(i + 1) % 3].n))
+      return SGQA_ERR_INVALID_ARG;
+  }
   PlanArgs a;
   a.pd = pd;
   a.mass = mass_pages;

@@ -623,7 +623,8 @@ SGQA_API int sgqa_paged_mass(const sgqa_paged_params* p, const void* Q, const vo
  * pos_pages NULL: an entry's index is its position.)  Writes n_moves [N][Hkv];
  * moves [N][Hkv][budget][2] (from, to), of which the first n_moves are written:
  * the i-th kept entry from `budget` on goes to the i-th dropped entry below it;
- * and kv_len_out [N] = min(kv_len, budget).  Only reads the cache.
+ * and kv_len_out [N] = min(kv_len, budget).  Only reads the cache.  The outputs
+ * overlap neither an input nor one another (INVALID_ARG).
  * 1 <= budget, sinks + recent <= budget, N * Hkv * budget below 2^31, N * Hkv up to 2^24;
  * mass_pages and pos_pages on 16-byte boundaries.
  * Device checks (SGQA_ERR_BOUNDS): kv_len outside [0, max_pages * page_size]

@@ -83,6 +83,25 @@ def test_verify_lengths_in_place_many(s):
 
 
 # ------------------------------------------------------------------ eviction
+@no_gpu
+@pytest.mark.parametrize("optional", [True, False])
+def test_plan_refuses_outputs_on_inputs(s, optional):
+    """(kv_len_out on next_pos, say, would change what other groups of the request take for
+    recent.)"""
+    n, hk, ps, pages, cols, budget = 3, 2, 16, 20, 4, 6
+    p = params(s, n_seqs=n, n_kv_heads=hk, page_size=ps, n_pages=pages, max_pages=cols)
+    inputs = dict(mass_pages=4 * pages * hk * ps, pos_pages=4 * pages * hk * ps, page_table=4 * n * cols,
+                  kv_len=4 * n, next_pos=4 * n)
+    outputs = dict(n_moves=4 * n * hk, moves=8 * n * hk * budget, kv_len_out=4 * n)
+    for o, b, at in clashes(inputs, outputs):
+        if not optional:
+            at.update(pos_pages=None, next_pos=None)
+            if b in ("pos_pages", "next_pos"):
+                continue
+        rc = s._lib.sgqa_evict_plan(ctypes.byref(p), budget, 1, 1, *at.values(), None, None)
+        assert rc == s.ERR_INVALID_ARG, (o, b)
+
+
 @gpu
 def test_plans_of_two_host_threads(s):
     """Tables of different widths, planned from two threads at once: the shared memory that one
