@@ -364,7 +364,9 @@ __global__ void __launch_bounds__(MT, 4) k_evict_move(const __grid_constant__ Mo
   const int s = unit / a.pd.Hkv, g = unit - s * a.pd.Hkv;
   const int lane = lane_id();
   int n = a.n_moves[unit];
-  if (n < 0 || n > a.budget) {
+  // (targets are distinct, so there are no more moves than places; the index below stays far
+  // from 2^31 so)
+  if (n < 0 || n > min(a.budget, a.pd.cap)) {
     if (part == 0 && threadIdx.x == 0) report(a.status, SGQA_ERR_BOUNDS, 381);
     n = 0;
   }

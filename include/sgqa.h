@@ -643,7 +643,7 @@ SGQA_API int sgqa_evict_plan(const sgqa_paged_params* p, int32_t budget, int32_t
  * (sgqa_evict_plan's are).  A page that several requests share changes for all
  * of them, so a request that is cut down has pages of its own.  moves on an 8-byte boundary, the pools on 16-byte
  * ones.  Device checks (SGQA_ERR_BOUNDS): an n_moves outside
- * [0, budget], a move from or to a place outside the table's range or a page
+ * [0, budget] or above max_pages * page_size, a move from or to a place outside the table's range or a page
  * outside the pool, are skipped. */
 SGQA_API int sgqa_evict_move(const sgqa_paged_params* p, int32_t budget,
                              const int32_t* page_table, const int32_t* n_moves,

@@ -138,3 +138,23 @@ def test_plans_of_two_host_threads(s):
     for a, b in zip(*got):
         assert torch.equal(a, b)
     assert (got[0][0] == kv - budget).all()
+
+
+@gpu
+def test_move_counts_above_the_table(s):
+    """More moves than the table has places cannot be distinct: none is carried out, even
+    where the budget would allow them."""
+    ps, cols, budget = 8, 4, 100
+    p = params(s, n_seqs=2, max_tokens=0, n_q_heads=1, n_kv_heads=1, page_size=ps, n_pages=8, max_pages=cols)
+    K = torch.randn(8, 1, ps, 64).to(torch.bfloat16).cuda()
+    V = K.flip(0).contiguous()
+    table = torch.arange(8, dtype=torch.int32).view(2, cols).cuda()
+    moves = torch.zeros(2, 1, budget, 2, dtype=torch.int32)
+    moves[:, 0, :, 0], moves[:, 0, :, 1] = 31, torch.arange(budget)
+    counts = torch.tensor([[33], [1]], dtype=torch.int32)
+    k, v, st = K.clone(), V.clone(), s.new_status()
+    s.sgqa_evict_move(p, table, counts.cuda(), moves.cuda(), k, v, budget, status=st)
+    assert s.read_status(st) == (s.ERR_BOUNDS, 381)
+    for x, y in ((k, K), (v, V)):
+        y[4, 0, 0] = y[7, 0, 7]  # the second request's one move
+        assert torch.equal(x, y)
