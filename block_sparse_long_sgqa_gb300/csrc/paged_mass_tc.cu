@@ -215,6 +215,46 @@ __device__ __forceinline__ bool walk(const TcArgs& a, int64_t total, Publish pub
   return true;
 }
 
+// The sum of a tile of rows for one key, row by row, where the sum from the products is NaN:
+// a row whose lse is -infinity adds nothing, whatever it or the key holds, and once -infinity
+// has been added to a product that is not finite nothing tells whose the NaN was.  (One of a row
+// that counts is found here too, and ends the loop.)  At most 128 rows, some 50 us, far from
+// the waits' limit.  Out of line and for NaN only: leaving such rows out where the products are
+// read cost single tokens 16 % (176 to 204 us), a flag that led to a second copy of that
+// code 11 %; this costs 0.3 to 0.5 % of both.
+template <int D>
+__device__ __noinline__ float again(const TcArgs& a, int at, int row0, int rows, int pos0, int key) {
+  const int g = (int)((unsigned)at / (unsigned)a.pd.ps % (unsigned)a.pd.Hkv), G = a.pd.G;
+  uint4 k[D / 8];
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i)
+    k[i] = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.K) + (int64_t)at * D)[i];
+  float sum = 0.0f;
+  for (int t = 0; t < rows; ++t) {
+    if (!sees(a, pos0 + t, key)) continue;
+    for (int h = g * G; h < g * G + G; ++h) {
+      const float l = a.lse[(int64_t)h * a.pd.T + row0 + t];
+      if (l == -__int_as_float(0x7f800000)) continue;
+      const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.Q) +
+                                                      (int64_t)(row0 + t) * a.pd.qs + (int64_t)h * D);
+      float s = 0.0f;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        const uint4 x = q[i], y = k[i];
+        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          s = fmaf(__uint_as_float(xs[j] << 16), __uint_as_float(ys[j] << 16), s);
+          s = fmaf(__uint_as_float(xs[j] & 0xffff0000u), __uint_as_float(ys[j] & 0xffff0000u), s);
+        }
+      }
+      sum += exp2f(fmaf(s, a.sl2, -l * 1.4426950408889634f));
+      if (sum != sum) return sum;
+    }
+  }
+  return sum;
+}
+
 template <int D>
 __global__ void __launch_bounds__(NTHREADS, 1)
     k_mass(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap ms,
@@ -435,7 +475,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           // three terms, each the bf16 nearest to what is left; a row that saw nothing adds
-          // nothing (2 to the -inf)
+          // nothing (2 to the -inf, or by again() where its product is not finite)
           const float v = l[x] == ninf ? ninf : -(l[x] * a.inv);
           const float hi = __bfloat162float(__float2bfloat16_rn(v));
           const bool more = fabsf(hi) < -ninf;
@@ -556,7 +596,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     // A piece as this thread needs it, with what its key's entry holds: asked for when the
     // piece before it is begun, if it is known by then.
     struct Mine {
-      int key, kv, first, i0, ntok, slot, end, here, at, pos;
+      int key, kv, first, i0, row0, ntok, slot, end, here, at, pos;
       float old;
     };
     auto take = [&](int i) -> Mine {
@@ -566,6 +606,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       m.kv = pc.kv;
       m.first = pc.first;
       m.i0 = pc.i0;
+      m.row0 = pc.row0;
       m.ntok = pc.ntok;
       m.slot = pc.slot;
       m.end = pc.end;
@@ -690,7 +731,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
         float s0, s1;
         f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), s0, s1);
-        sum += s0 + s1;
+        float add = s0 + s1;
+        if (__any_sync(FULL, add != add)) {
+          if (add != add && m.at >= 0)
+            add = again<D>(a, m.at, m.row0 + t, rows, m.first + m.i0 + t, m.key);
+          __syncwarp();
+        }
+        sum += add;
       }
       if (!ok) break;
       if (m.here) {

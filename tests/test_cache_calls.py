@@ -7,7 +7,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_cache_ops import VERIFIES, VerifyCase, dev
+from test_cache_ops import VERIFIES, MassCase, VerifyCase, dev
 from test_paged import params, status_of
 
 gpu = pytest.mark.gpu
@@ -158,3 +158,57 @@ def test_move_counts_above_the_table(s):
     for x, y in ((k, K), (v, V)):
         y[4, 0, 0] = y[7, 0, 7]  # the second request's one move
         assert torch.equal(x, y)
+
+
+# ------------------------------------------------------- accumulated weights
+def entries_of(c, i, j):
+    """Mask of the entries of cached positions j of request i, in every group."""
+    m = np.zeros(c.old.shape, bool)
+    m[c.b.table[i, j // c.ps], :, j % c.ps] = True
+    return m
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("name", ["decode", "chunks", "heads", "window", "full", "observe", "many", "cut",
+                                  "mix", "mix_window", "mix_full", "mix_ends", "wide"])
+def test_mass_leaves_out_marked_rows(s, name, value, dtype):
+    """Rows whose lse is -infinity add nothing, whatever they hold, and neither do keys that only
+    such rows see."""
+    c = MassCase(s, name, dtype, seed=3)
+    rng = np.random.default_rng(4)
+    out = rng.random(c.lse.shape) < 0.2
+    Q, K = c.t["Q"], c.t["K_pages"]
+    for i, (a, n) in enumerate(zip(c.q, c.kv)):
+        if c.causal and 1 < a <= n:  # the last token, and with it the last key
+            out[:, c.q_start[i + 1] - 1] = True
+            K[int(c.b.table[i, (n - 1) // c.ps]), :, (n - 1) % c.ps] = value
+    c.lse[out] = -np.inf
+    c.t["lse"].copy_(torch.tensor(c.lse))
+    Q[torch.tensor(out.T.copy()).cuda()] = value
+    for _ in range(3):
+        assert c.run(s) == s.OK
+        c.check()
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("name", ["decode", "cut", "mix", "mix_full", "mix_ends_few", "many"])
+def test_marked_rows_change_no_other_request(s, name, dtype):
+    """One row marked in one request: the others' entries keep their bits, and a repeated call
+    repeats all."""
+    c = MassCase(s, name, dtype)
+    assert c.run(s) == s.OK
+    before = c.t["mass_out"].clone()
+    c.t["lse"][0, int(c.q_start[1]) - 1] = -float("inf")
+    first = None
+    for _ in range(10):
+        c.t["mass_out"].fill_(77.0)
+        assert c.run(s) == s.OK
+        got = c.t["mass_out"].clone()
+        first = got if first is None else first
+        assert torch.equal(got.view(torch.int32), first.view(torch.int32))
+    mine = torch.tensor(entries_of(c, 0, np.arange(c.kv[0]))).cuda()
+    assert torch.equal(got[~mine].view(torch.int32), before[~mine].view(torch.int32))
+    assert not torch.equal(got[mine], before[mine])
