@@ -279,7 +279,27 @@ SGQA_API int sgqa_paged_mass(const sgqa_paged_params* p, const void* Q, const vo
     return SGQA_ERR_INVALID_ARG;
   if (!aligned16(Q) || !aligned16(K_pages)) return SGQA_ERR_ALIGNMENT;
   if (a.pd.scale < 0x1p-64f) return SGQA_ERR_UNSUPPORTED;  // (lse / scale has to be finite)
-  if (ws == nullptr || ws_bytes < sgqa_mass_workspace_bytes(p)) return SGQA_ERR_WORKSPACE;
+  const size_t need = sgqa_mass_workspace_bytes(p);
+  if (ws == nullptr || ws_bytes < need) return SGQA_ERR_WORKSPACE;
+  // What is written on what is read: every block goes by the lengths for itself, and finds other
+  // work than its neighbours if they change under it.
+  const size_t elem = (size_t)a.pd.elem, seqs = (size_t)a.pd.N * 4, toks = (size_t)a.pd.T * 4;
+  const size_t entries = (size_t)a.pd.n_pages * a.pd.Hkv * a.pd.ps;
+  const size_t rows = a.pd.T ? ((size_t)(a.pd.T - 1) * a.pd.qs + (size_t)a.pd.H * a.pd.d) * elem : 0;
+  const struct {
+    const void* p;
+    size_t n;
+  } outs[3] = {{mass_out, entries * 4}, {pos_pages, entries * 4}, {ws, need}};
+  for (int i = 0; i < 3; ++i) {
+    const auto& o = outs[i];
+    if (overlap(o.p, o.n, Q, rows) || overlap(o.p, o.n, K_pages, entries * a.pd.d * elem) ||
+        overlap(o.p, o.n, page_table, seqs * a.pd.max_pages) ||
+        overlap(o.p, o.n, q_start, seqs + 4) || overlap(o.p, o.n, kv_len, seqs) ||
+        overlap(o.p, o.n, lse, toks * a.pd.H) || overlap(o.p, o.n, positions, toks) ||
+        ((i != 0 || mass_out != mass_in) && overlap(o.p, o.n, mass_in, entries * 4)) ||
+        overlap(o.p, o.n, outs[(i + 1) % 3].p, outs[(i + 1) % 3].n))
+      return SGQA_ERR_INVALID_ARG;
+  }
   // windows and lengths end at cap: the sums of both stay in 32 bits
   if (a.pd.window > a.pd.cap) a.pd.window = a.pd.cap;
   a.Q = Q;

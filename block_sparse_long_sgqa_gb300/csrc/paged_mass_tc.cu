@@ -195,9 +195,10 @@ __device__ __forceinline__ bool walk(const TcArgs& a, int64_t total, Publish pub
           pc.end = 0;
           if (t1 - t0 < units) {
             pc.slot = 2 * blockIdx.x + (t0 > 0 ? 0 : 1);
-            if (t0 == 0) {  // begun here, continued by the CTAs up to the last tile's
-              int e = blockIdx.x;
-              while (before(min(total, share * (e + 1))) < units) ++e;
+            if (t0 == 0) {
+              // begun here, continued by the CTAs up to that of the item's last tile (of those
+              // there are, should the lengths have changed since the line was laid)
+              const int e = (int)min((at + (int64_t)(units - 1) * a.tpm) / share, (int64_t)kGrid - 1);
               *rec = make_int4(pc.s, pc.g, pc.k0, e - (int)blockIdx.x + 1);
             }
           }

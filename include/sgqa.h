@@ -597,7 +597,8 @@ SGQA_API int sgqa_rope_append(const sgqa_paged_params* p, const sgqa_rope_table*
  * what the row sees NaN.  observe > 0: only the last `observe` tokens of each
  * request add (every position's entry is written all the same).  Positions
  * that no adding row sees add nothing, whatever their keys hold.  mass_in and
- * mass_out may be one buffer; entries of pages that hold no cached position are
+ * mass_out may be one buffer; otherwise outputs and workspace overlap neither an
+ * input nor one another (INVALID_ARG).  Entries of pages that hold no cached position are
  * not written.  positions (max_tokens) and pos_pages (both or neither NULL):
  * the entry of each new token gets positions[t], in every group.
  * bf16 runs on the tensor cores; sums in fp32.  Results do not depend on

@@ -168,6 +168,30 @@ def entries_of(c, i, j):
     return m
 
 
+@no_gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("with_pos", [True, False])
+def test_mass_refuses_outputs_on_inputs(s, dtype, with_pos):
+    n, t, h, hk, d, ps, pages, cols, e = 3, 11, 8, 2, 64, 16, 20, 4, 2 if dtype == "bf16" else 4
+    p = params(s, n_seqs=n, max_tokens=t, n_q_heads=h, n_kv_heads=hk, page_size=ps, n_pages=pages,
+               max_pages=cols, dtype=s.BF16 if e == 2 else s.FP32, q_stride=(h + 4) * d)
+    need = s.mass_workspace_bytes(p)
+    entries = pages * hk * ps
+    inputs = dict(Q=((t - 1) * (h + 4) + h) * d * e, K_pages=entries * d * e, page_table=4 * n * cols,
+                  q_start=4 * n + 4, kv_len=4 * n, lse=4 * h * t, mass_in=4 * entries, positions=4 * t)
+    outputs = dict(mass_out=4 * entries, pos_pages=4 * entries, ws=need)
+    order = ("Q", "K_pages", "page_table", "q_start", "kv_len", "lse", "mass_in", "mass_out", "positions",
+             "pos_pages", "ws")
+    for o, b, at in clashes(inputs, outputs, allowed=[("mass_out", "mass_in")]):
+        if not with_pos:
+            if "pos_pages" in (o, b) or b == "positions":
+                continue
+            at.update(positions=None, pos_pages=None)
+        a = [at[k] for k in order]
+        rc = s._lib.sgqa_paged_mass(ctypes.byref(p), *a[:6], 0, *a[6:], need, None, None)
+        assert rc == s.ERR_INVALID_ARG, (o, b)
+
+
 @gpu
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("value", [float("nan"), float("inf")])
