@@ -278,7 +278,8 @@ SGQA_API int sgqa_paged_mass(const sgqa_paged_params* p, const void* Q, const vo
       (a.pd.T > 0 && (Q == nullptr || lse == nullptr)))
     return SGQA_ERR_INVALID_ARG;
   if (!aligned16(Q) || !aligned16(K_pages)) return SGQA_ERR_ALIGNMENT;
-  if (a.pd.scale < 0x1p-64f) return SGQA_ERR_UNSUPPORTED;  // (lse / scale has to be finite)
+  // (lse / scale has to be finite, where the lse goes through the product)
+  if (a.pd.dtype == SGQA_BF16 && a.pd.scale < 0x1p-64f) return SGQA_ERR_UNSUPPORTED;
   const size_t need = sgqa_mass_workspace_bytes(p);
   if (ws == nullptr || ws_bytes < need) return SGQA_ERR_WORKSPACE;
   // What is written on what is read: every block goes by the lengths for itself, and finds other

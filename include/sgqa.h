@@ -604,7 +604,7 @@ SGQA_API int sgqa_rope_append(const sgqa_paged_params* p, const sgqa_rope_table*
  * bf16 runs on the tensor cores; sums in fp32.  Results do not depend on
  * scheduling: two calls on the same inputs agree bit for bit.  Device checks as
  * in sgqa_paged_attn (a page number outside the pool: its entries are skipped).
- * softmax_scale, if given, is at least 2^-64 (SGQA_ERR_UNSUPPORTED otherwise).
+ * softmax_scale, if given, is at least 2^-64 in bf16 (SGQA_ERR_UNSUPPORTED otherwise).
  * Requests that share pages: the shared entries belong to one of them, and its
  * calls must not overlap the others'.  Workspace: sgqa_mass_workspace_bytes(p);
  * calls that may overlap need one each. */

@@ -7,6 +7,7 @@ import numpy as np
 import pytest
 import torch
 
+import paged_ref as ref
 from test_cache_ops import VERIFIES, MassCase, VerifyCase, dev
 from test_paged import params, status_of
 
@@ -236,3 +237,21 @@ def test_marked_rows_change_no_other_request(s, name, dtype):
     mine = torch.tensor(entries_of(c, 0, np.arange(c.kv[0]))).cuda()
     assert torch.equal(got[~mine].view(torch.int32), before[~mine].view(torch.int32))
     assert not torch.equal(got[mine], before[mine])
+
+
+@gpu
+@pytest.mark.parametrize("dtype,scale", [("bf16", 2.0 ** -64), ("bf16", 1e-6), ("bf16", 0.02), ("bf16", 1.0),
+                                         ("bf16", 3.0), ("fp32", 1e-30), ("fp32", 2.0 ** -64), ("fp32", 0.02),
+                                         ("fp32", 1.0), ("fp32", 3.0)])
+@pytest.mark.parametrize("name", ["decode", "chunks", "cut", "window"])
+def test_mass_other_scales(s, name, dtype, scale):
+    """Scales from one under which all keys weigh the same to one under which one key has it all."""
+    c = MassCase(s, name, dtype, seed=6)
+    c.scale = float(np.float32(scale))
+    _, lse, _, _, _ = ref.attention(c.Q64, c.K64, np.zeros_like(c.K64), c.ps, c.b.table, c.q_start, c.kv,
+                                    c.scale, c.causal, c.window, dtype == "bf16")
+    c.lse = lse.astype(np.float32)
+    c.t["lse"].copy_(torch.tensor(c.lse))
+    c.p.softmax_scale = scale
+    assert c.run(s) == s.OK
+    c.check()
