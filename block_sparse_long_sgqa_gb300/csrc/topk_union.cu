@@ -1385,7 +1385,7 @@ int launch_topk_union_layout(const Dims& dm, const float* scores, int64_t q_begi
   const size_t row_smem = (size_t)ROW_WARPS * WARP_BYTES;
   // tiles: bitmask + word prefix + member masks (shared while they fit)
   const size_t fixed = (size_t)(((a.nwords + 3) & ~3) + ((a.nwords + 1 + 3) & ~3)) * 4;
-  const size_t budget = 200 * 1024;
+  constexpr size_t budget = 200 * 1024;
   if (fixed + 1024 > budget) return SGQA_ERR_UNSUPPORTED;
   const int64_t u_max = std::min<int64_t>((int64_t)dm.W * dm.Ks, dm.nblk);  // slots of a tile
   // (the lists are read twice, from L2; a small footprint keeps many CTAs per SM)
@@ -1393,10 +1393,12 @@ int launch_topk_union_layout(const Dims& dm, const float* scores, int64_t q_begi
   const int64_t mask_pairs =
       std::min<int64_t>(std::min<int64_t>(u_max, 4096), (int64_t)(mask_budget / 8));
   const size_t union_smem = fixed + (size_t)mask_pairs * 8;
+  // (the limit belongs to the process: always the most that a call can ask for, so that another
+  // thread's smaller call does not lower it before this one's launch)
   if (cudaFuncSetAttribute(k_topk_rows, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            (int)row_smem) != cudaSuccess ||
       cudaFuncSetAttribute(k_tile_union, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)union_smem) != cudaSuccess)
+                           (int)budget) != cudaSuccess)
     return SGQA_ERR_CUDA;
   log_begin(SGQA_K_TOPK_UNION, st);
   k_topk_rows<<<(unsigned)row_ctas, ROW_WARPS * 32, row_smem, st>>>(a);
