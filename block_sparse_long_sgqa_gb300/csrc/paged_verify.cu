@@ -6,7 +6,7 @@
 // first token whose cumulative weight exceeds u times the total.  That takes one pass over
 // the row (two rows, with D), shared by a cluster of CTAs: each sums its part of the row,
 // the parts' sums go round through distributed shared memory, and the one CTA in whose
-// part the place lies looks at the 1/16 of it (one warp's range) once more.
+// part the place lies looks at the 1/8 of it (one warp's range) once more.
 //
 // Borders between tokens lie about 1/vocab apart, so the sums have to be much finer than
 // fp32: pairs of fp32 numbers (47 bits), w = P - D exactly as rounded value and

@@ -8,7 +8,8 @@ import pytest
 import torch
 
 import paged_ref as ref
-from test_cache_ops import VERIFIES, MassCase, VerifyCase, dev
+from test_cache_ops import (PLANS, VALUES, VERIFIES, MassCase, VerifyCase, check_plan, dev,
+                            plan_case)
 from test_paged import params, status_of
 
 gpu = pytest.mark.gpu
@@ -68,13 +69,10 @@ def test_verify_lengths_in_place(s, name):
 
 
 @gpu
-def test_verify_lengths_in_place_many(s):
+def test_verify_lengths_in_place_many(s, monkeypatch):
     """The same with more requests than fit the SMs at a time."""
-    VERIFIES["crowd"] = ([2] * 400, 20000, True, "bf16", 0)
-    try:
-        c = VerifyCase(s, "crowd")
-    finally:
-        del VERIFIES["crowd"]
+    monkeypatch.setitem(VERIFIES, "crowd", ([2] * 400, 20000, True, "bf16", 0))
+    c = VerifyCase(s, "crowd")
     c.kv = np.diff(c.q_start).astype(np.int32)
     for _ in range(5):
         kv = dev(c.kv).clone()
@@ -101,6 +99,27 @@ def test_plan_refuses_outputs_on_inputs(s, optional):
                 continue
         rc = s._lib.sgqa_evict_plan(ctypes.byref(p), budget, 1, 1, *at.values(), None, None)
         assert rc == s.ERR_INVALID_ARG, (o, b)
+
+
+CLUSTERS = {  # blocks of a (request, group) by the table's places and by how many there are of them
+    "four_idle": ([20000, 30, 16400], 2, 64, 3000, 50, 4, 0),           # 20032 places, 6 of them
+    "two_full": ([32800, 5000] + [40] * 36, 4, 32, 4096, 7, 3, 0),      # 32800 places, 152
+    "four_full": ([66000, 300] + [40] * 36, 4, 32, 10000, 0, 0, 0),     # 66016 places, 152
+    "eight_full": ([140000, 9] + [40] * 36, 4, 64, 20000, 100, 9, 0),   # 140032 places, 152
+}
+
+
+@gpu
+@pytest.mark.parametrize("with_pos", [True, False])
+@pytest.mark.parametrize("values", VALUES)
+@pytest.mark.parametrize("name", CLUSTERS)
+def test_plan_clusters(s, name, values, with_pos, monkeypatch):
+    monkeypatch.setitem(PLANS, name, CLUSTERS[name])
+    _, p, t, want = plan_case(s, name, values, with_pos=with_pos)
+    st = s.new_status()
+    s.sgqa_evict_plan(p, **t, status=st)
+    assert status_of(s, st) == s.OK
+    check_plan(t, want)
 
 
 @gpu
