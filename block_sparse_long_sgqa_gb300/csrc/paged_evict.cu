@@ -10,9 +10,13 @@
 // requests, share a (request, group) among a cluster of CTAs, which adds up its histograms
 // through distributed shared memory.
 //
-// What bounds it: instructions (61 % of the issue slots over the whole call) and the steps'
-// barriers; 64 requests of 5K to 32K entries, 8 groups: 49 us where reading weights and
-// positions takes 10.  Single pages over the budget are bound by the call.
+// What bounds it: instructions (58 % of the issue slots while a block runs, 43 % over the whole
+// call, which ends on the SMs with the longest requests) and the steps' barriers; 64 requests of
+// 5K to 32K entries, 8 groups: 49 us where reading weights and positions takes 10.  Single pages
+// over the budget are bound by the call.  Both with page tables no wider than the longest
+// request: the host picks the form by that width, since it does not see the lengths, and short
+// caches in a table of 256K positions take 446 us in place of 49 (single pages 60 in place of 8),
+// in one of 1M 679 (76).
 //
 // Order among the kept entries has no meaning to attention, so entries below the budget
 // stay where they are: a step that drops one page of entries moves about a page of rows,
@@ -492,10 +496,11 @@ SGQA_API int sgqa_evict_plan(const sgqa_paged_params* p, int32_t budget, int32_t
   a.budget = budget;
   a.recent = recent;
   a.sinks = sinks;
-  // CTAs of a cluster: as few as hold the keys that a request can have, since a cluster's
-  // barriers and the histograms of the others cost more than they share out (64 requests of
-  // 5K to 32K entries, 8 groups: 59 us with one CTA, 81 with two, 153 with four, before both
-  // got faster); more where the call would leave SMs idle and a CTA keeps 4096 keys
+  // CTAs of a cluster: as few as hold the keys that a request can have (by the width of the
+  // table, the only bound on the lengths that the host knows), since a cluster's barriers and
+  // the histograms of the others cost more than they share out (64 requests of 5K to 32K
+  // entries, 8 groups: 59 us with one CTA, 81 with two, 153 with four, before both got
+  // faster); more where the call would leave SMs idle and a CTA keeps 4096 keys
   int c = 1;
   while (c < kMaxCluster && ((int64_t)c * kMostKeys < pd.cap ||
                              ((int64_t)pd.N * pd.Hkv * c < 152 && (int64_t)c * 8192 < pd.cap)))

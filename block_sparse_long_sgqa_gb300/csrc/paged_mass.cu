@@ -19,7 +19,10 @@ namespace {
 constexpr int NT = 256;
 constexpr int KB = 64, RB = 64;  // keys and rows of a tile
 constexpr int FR = 8;            // rows of a turn of the few
-// Rows of an item up to which it goes the way of the few.
+// Rows of an item up to which it goes the way of the few.  16 requests over 3000 keys, 4 groups,
+// that way and the other: 8 rows 57 and 145 us, 24 rows 90 and 152, 48 rows 140 and 165, 64 rows
+// 173 and 172; at head dim 64, 24 rows 68 and 90, 40 rows 94 and 94, 64 rows 132 and 98.  24 is on
+// the few's side of both.
 constexpr int kFew = 24;
 
 template <int D>

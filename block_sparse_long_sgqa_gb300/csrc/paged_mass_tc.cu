@@ -23,8 +23,8 @@
 // (with four groups and 32 columns at a time a product waited for the exponentials of the
 // one before: 1011 us on the chunks below).
 //
-// What bounds it.  64 single tokens over 500 to 32K keys, 8 groups: the keys' bytes, 176 us,
-// 6.2 TB/s.  Chunks of 1024 and 2048 tokens over 4K to 16K keys, 64 heads: 972 us, 1150
+// What bounds it.  64 single tokens over 500 to 32K keys, 8 groups: the keys' bytes, 178 us,
+// 6.2 TB/s.  Chunks of 1024 and 2048 tokens over 4K to 16K keys, 64 heads: 975 us, 1145
 // TFLOP/s; a tile of 256 keys by 128 rows takes 2200 cycles, 1200 of them products (the
 // tensor pipe is 54 % active) and 1024 exponentials.  Neither is the limit by itself: with
 // one product in nine the time is the same, with one exponential in eight it is 1650
@@ -42,7 +42,10 @@ constexpr int BM = 128;            // rows of a tile, at most
 constexpr int NTHREADS = 384;
 constexpr int kGrid = 152;         // one CTA per SM
 constexpr int NPC = 4;             // pieces in the ring
-constexpr int kWhole = 8;          // tiles of rows up to which an item is not cut
+// Tiles of rows up to which an item is not cut.  Three requests of 100 tokens (7 tiles) over 8K to
+// 16K keys: 65 us uncut, 68 cut (a limit of 2); of 300 tokens (19 tiles): 160 us cut (limits of 2, 8
+// and 16), 173 uncut (32).
+constexpr int kWhole = 8;
 constexpr int kOver = 2;           // an item's keys, in tiles of rows
 
 template <int D>
@@ -219,8 +222,9 @@ __device__ __forceinline__ bool walk(const TcArgs& a, int64_t total, Publish pub
 // The sum of a tile of rows for one key, row by row, where the sum from the products is NaN:
 // a row whose lse is -infinity adds nothing, whatever it or the key holds, and once -infinity
 // has been added to a product that is not finite nothing tells whose the NaN was.  (One of a row
-// that counts is found here too, and ends the loop.)  At most 128 rows, some 50 us, far from
-// the waits' limit.  Out of line and for NaN only: leaving such rows out where the products are
+// that counts is found here too, and ends the loop.)  At most 128 rows, some 0.1 ms, far from
+// the waits' limit: the chunks above take 104 ms with a NaN in one left-out row of every tile, 975 us
+// with finite rows left out.  Out of line and for NaN only: leaving such rows out where the products are
 // read cost single tokens 16 % (176 to 204 us), a flag that led to a second copy of that
 // code 11 %; this costs 0.3 to 0.5 % of both.
 template <int D>
@@ -662,6 +666,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           if (lane == 0) mbar_arrive(&s_empty[half * 2 + buf]);
         };
         uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+        // (of groups that divide 128: other tiles have fewer rows, and go the second way; chunks
+        // of 28 heads on 4 486 us, of 32 on 4 494)
         const bool whole = __all_sync(FULL, c0 == 0 && c1 == BM);
         if (whole) {
           uint32_t v[128];

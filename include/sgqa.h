@@ -496,6 +496,11 @@ SGQA_API int sgqa_paged_attn(const sgqa_paged_params* p, const void* Q, const vo
  *   PARTS:  theta_i (w + (1 - w) / factor), w = clamp((n_i - low) / (high -
  *           low), 0, 1) with n_i = orig_len theta_i / (2 pi), the turns that
  *           pair i makes in the trained context; a = 0.1 ln(factor) + 1.
+ *           The rule known as NTK-by-parts or YaRN, as it was published: the ramp
+ *           is linear in the turns (its constants: low = 1, high = 32).  Where a
+ *           checkpoint wants no amplitude, amplitude = 1; where its ramp is linear
+ *           in the pair's index, between two pairs computed from low and high,
+ *           its frequencies differ in between and are passed as theta.
  * The angle's place in its turn is the exact product of the position and a
  * 64-bit fixed-point frequency (turns per position), so it is as good at the
  * last position as at the first; sines and cosines are fp32. */
@@ -593,8 +598,10 @@ SGQA_API int sgqa_rope_append(const sgqa_paged_params* p, const sgqa_rope_table*
  * over the request's tokens t that see j (causal and window of p, as in
  * sgqa_paged_attn) and the heads h of the group of exp(scale Q[t][h] . K[j] -
  * lse[h][t]).  lse [H][max_tokens] is sgqa_paged_attn's; a row whose lse is
- * -infinity saw nothing and adds nothing, a NaN there makes the weights of
- * what the row sees NaN.  observe > 0: only the last `observe` tokens of each
+ * -infinity saw nothing and adds nothing, whatever it holds (in bf16, where
+ * that is a NaN or infinity, its tile is added up again on the CUDA cores, some
+ * hundred times slower), a NaN there makes the weights of what the row sees
+ * NaN.  observe > 0: only the last `observe` tokens of each
  * request add (every position's entry is written all the same).  Positions
  * that no adding row sees add nothing, whatever their keys hold.  mass_in and
  * mass_out may be one buffer; otherwise outputs and workspace overlap neither an
